@@ -74,6 +74,8 @@ typedef enum qmoe_status {
 /* flags OR-ed into the device status word */
 #define QMOE_DEV_BAD_EXPERT 0x1  /* an expert id outside [0, num_experts) was skipped */
 #define QMOE_DEV_TIMEOUT 0x2     /* a pipeline wait gave up; outputs are invalid */
+#define QMOE_DEV_BAD_PAGE 0x4    /* a page id outside the cache, or a length beyond the page table */
+#define QMOE_DEV_BAD_TOKEN 0x8   /* a token id outside the vocabulary was skipped */
 
 /* One affine-quantized matrix (or a stack of equally-shaped matrices).
  *   packed: uint32 [rows][cols*bits/32]   (16-byte aligned)
@@ -468,6 +470,195 @@ qmoe_status moe_prefill_qgemm(const qmoe_moe_layer *L, const uint16_t *x, int32_
                               const int32_t *idx, const float *weights, int32_t top_k,
                               uint16_t *y, void *workspace, size_t workspace_bytes,
                               int32_t *status_dev, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Between the projections of a layer: rotary positions, a paged K/V cache and
+ * the attention that reads it (TurboFieldfare article: an fp16 cache of 25
+ * sliding-window and 5 full-attention layers; uzu deep dive: K/V storage).
+ *
+ * 16-bit tensors here are fp16 or bf16 (QMOE_F16, QMOE_BF16; one type per
+ * call) and may be strided: strides count elements, a head's elements follow
+ * each other.
+ *
+ * qmoe_kv_cache: one layer's cache, num_pages pages of page_size tokens each
+ *   (any size).  K/V head h of slot s of page p starts at element
+ *   p*page_stride + s*token_stride + h*head_stride of both k and v, so pages
+ *   may hold [token][head][dim] or [head][token][dim].  k, v 16-byte aligned,
+ *   strides multiples of 8, head_dim a multiple of 8, at most 256.
+ * qmoe_kv_batch: the step's sequences, all in device memory.  Sequence b's
+ *   new tokens are rows q_start[b] .. q_start[b+1] of the step's tensors
+ *   (q_start ascending; rows outside all sequences are left as they were);
+ *   kv_len[b] is its cached length WITH the new tokens, so its row i is at
+ *   position kv_len[b] - n_b + i; cached token j lies in page
+ *   page_table[b*max_pages + j/page_size], slot j % page_size.  Entries
+ *   behind a sequence's last page are not read.  `tokens` is the number of
+ *   rows of the tensors; max_new an upper bound of n_b that only chooses the
+ *   kernel (0: none known).  Lengths are read by the kernels: a captured graph
+ *   replays with new ones.  A page id outside the cache, and a length beyond
+ *   the page table, raise QMOE_DEV_BAD_PAGE: keys and values of such a page
+ *   read as zeros and are not stored, the length is cut.
+ * ------------------------------------------------------------------------- */
+#define QMOE_F16 0
+#define QMOE_BF16 1
+#define QMOE_F32 2
+
+typedef struct qmoe_kv_cache {
+    void *k;
+    void *v;
+    int64_t page_stride, token_stride, head_stride;
+    int32_t num_pages, page_size, kv_heads, head_dim;
+    int32_t dtype;
+} qmoe_kv_cache;
+
+typedef struct qmoe_kv_batch {
+    const int32_t *page_table;
+    const int32_t *q_start;
+    const int32_t *kv_len;
+    int32_t batch, max_pages, tokens, max_new;
+} qmoe_kv_batch;
+
+/* Rotary positions.  Pair i < rot_dim/2 of a head is (x[i], x[i + rot_dim/2])
+ * in the half layout, (x[2i], x[2i+1]) in the interleaved one; at position p
+ * it is turned by the angle p * inv_freq[i] and multiplied by `scale`;
+ * elements from rot_dim on are copied.  inv_freq: fp64 [rot_dim/2], device
+ * memory, 8-byte aligned; rot_dim even, 2..head_dim.
+ * rope_frequencies fills such a table in HOST memory:
+ *   QMOE_ROPE_PLAIN   f_i = base^(-2i/rot_dim)
+ *   QMOE_ROPE_LINEAR  f_i / factor (positions interpolated)
+ *   QMOE_ROPE_BASE    base * factor^(rot_dim/(rot_dim-2)) in place of base
+ *                     (the lowest frequency is divided by factor, the highest kept)
+ *   QMOE_ROPE_BANDS   by how often a pair turns over the trained length,
+ *                     n_i = trained f_i / (2 pi): f_i where n_i >= high, f_i /
+ *                     factor where n_i <= low, between them the blend of the
+ *                     two linear in n_i
+ *   QMOE_ROPE_RAMP    the same two ends with the blend linear in i between the
+ *                     pairs that turn `high` and `low` times (rounded outwards
+ *                     to whole pairs); *scale = 0.1 ln(factor) + 1
+ * and *scale (1 but for RAMP).  trained, low, high are read by the last two
+ * only.  INVALID_ARG: rot_dim odd or < 2 (BASE: < 4), base <= 1, factor < 1,
+ * trained < 1 or not 0 < low < high. */
+#define QMOE_ROPE_HALF 0
+#define QMOE_ROPE_INTERLEAVED 1
+#define QMOE_ROPE_PLAIN 0
+#define QMOE_ROPE_LINEAR 1
+#define QMOE_ROPE_BASE 2
+#define QMOE_ROPE_BANDS 3
+#define QMOE_ROPE_RAMP 4
+
+typedef struct qmoe_rope {
+    const double *inv_freq;
+    int32_t rot_dim;
+    int32_t layout;
+    float scale;
+} qmoe_rope;
+
+qmoe_status rope_frequencies(int32_t rot_dim, double base, int32_t kind, double factor,
+                             int32_t trained, double low, double high, double *inv_freq,
+                             float *scale);
+
+/* out[t][h] = x[t][h] turned to position positions[t] (any sign: the negative
+ * position is the transpose, which is also the gradient).  x, out: [tokens]
+ * [heads][head_dim], 2-byte aligned, any strides; out may be x.  positions:
+ * int32 [tokens].  head_dim 2..1024. */
+qmoe_status rope_rotate(const qmoe_rope *rope, const void *x, int64_t x_token_stride,
+                        int64_t x_head_stride, int32_t dtype, int32_t tokens, int32_t heads,
+                        int32_t head_dim, const int32_t *positions, void *out,
+                        int64_t out_token_stride, int64_t out_head_stride, int32_t *status_dev,
+                        void *stream);
+
+/* One launch for a step's rows: k (turned) and v into their cache slots, and q
+ * (turned) to q_out.  q NULL: keys and values only (then heads is 0); rope
+ * NULL: nothing is turned, q must be NULL.  q_out may be q.  positions: int32
+ * [tokens], the positions of the rotation, or NULL: each row's place in its
+ * sequence.  A row whose slot is before 0 or beyond the page table is not
+ * stored and raises QMOE_DEV_BAD_PAGE.  q, k, v: the cache's type, 2-byte
+ * aligned, any strides (16-byte aligned rows and heads are faster). */
+typedef struct qmoe_rows {
+    void *data;
+    int64_t token_stride, head_stride;
+} qmoe_rows;
+
+qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
+                      const qmoe_rope *rope, const int32_t *positions, const qmoe_rows *q,
+                      const qmoe_rows *q_out, int32_t heads, const qmoe_rows *k,
+                      const qmoe_rows *v, int32_t *status_dev, void *stream);
+
+/* Attention of the new tokens over the cache (which already holds their own
+ * keys and values).  Row i of sequence b, at position p = kv_len[b] - n_b + i,
+ * sees key j when 0 <= j < kv_len[b], with `causal` j <= p, and with window >
+ * 0 j > p - window.  Query head h reads K/V head h / (heads / kv_heads):
+ *   s_j = scale * q.k_j;  softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *   out = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j)
+ * A row that sees nothing gets zeros and lse = -inf.  Keys and values that a
+ * row does not see do not reach it, infinities and NaNs included.
+ * q, out: [tokens][heads][head_dim] by strides, 16-byte aligned, strides
+ * multiples of 8, the cache's type; lse: fp32 [tokens][heads] or NULL.
+ * Scores, softmax statistics and sums are fp32; a weight enters the second
+ * product rounded to the cache's type, the output is rounded once.
+ * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device
+ * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every call
+ * leaves its counters zero again, so calls of any shape share it in turn, but
+ * not two that can run at the same time.  max_rows: the most rows of one
+ * sequence per K/V head in any call, max_new * heads / kv_heads (max_new 0:
+ * take `tokens`).
+ * UNSUPPORTED: head_dim not a multiple of 8 or above 256; tokens * heads / kv_heads
+ * above 2^30. */
+typedef struct qmoe_attn {
+    qmoe_rows q;
+    qmoe_rows out;
+    float *lse;
+    int32_t heads;
+    int32_t window;
+    int32_t causal;
+    float scale;
+    float softcap;
+} qmoe_attn;
+
+size_t attn_paged_workspace_bytes(int32_t head_dim, int64_t max_rows);
+qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
+                       const qmoe_kv_batch *batch, void *workspace, size_t workspace_bytes,
+                       int32_t *status_dev, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Between the vocabulary projection and the sampler: penalties for repeated
+ * tokens, biases and a grammar mask (Neurons page: repetition penalty of the
+ * sampler; uzu deep dive: grammar bit mask).  For token v of row r, x =
+ * logits[r][v] in fp32:
+ *   v in the row's history:  x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *   n > 0:  x = x - frequency[r] * n - presence[r],  n = how often v stands in
+ *           history[r][prompt_len[r] .. history_len[r])
+ *   x = x + the sum of bias[r][i] over all i with bias_ids[r][i] == v
+ *   bit v % 32 of mask[r][v / 32] clear:  x = -inf
+ * and out[r][v] = x rounded once to the logits' type (fp16, bf16 or fp32).
+ * A row whose mask allows nothing becomes all -inf.
+ * Each rule is left out where its pointer is NULL.  history: int32 [rows] of
+ * history_stride, max_history (< 2^20) of them at most; history_len (read by
+ * the kernel, cut at max_history), prompt_len (NULL: no prompt): int32 [rows].
+ * bias_ids: int32 [rows][max_bias], bias: fp32 the same, max_bias <= 1024.
+ * Ids of -1 are unused places; other ids outside the vocabulary are skipped
+ * and raise QMOE_DEV_BAD_TOKEN.  mask: uint32 [rows] of mask_stride words, or
+ * mask_stride 0: one mask for all rows.  logits, out: [rows][vocab] by row
+ * strides (elements); out may be logits.  rows 0..65535, vocab >= 1.
+ * ------------------------------------------------------------------------- */
+typedef struct qmoe_logit_rules {
+    const int32_t *history;
+    const int32_t *history_len;
+    const int32_t *prompt_len;
+    int64_t history_stride;
+    const float *repetition;
+    const float *presence;
+    const float *frequency;
+    const int32_t *bias_ids;
+    const float *bias;
+    const uint32_t *mask;
+    int64_t mask_stride;
+    int32_t max_history;
+    int32_t max_bias;
+} qmoe_logit_rules;
+
+qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, int64_t in_stride,
+                           int32_t dtype, int32_t rows, int32_t vocab, void *out,
+                           int64_t out_stride, int32_t *status_dev, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Format helpers (the packing reading of the "성능과 제약" section).

@@ -4,6 +4,8 @@
 // The operations and where the pages define them are listed in qmoe.h.  This
 // layer allocates nothing and never synchronises inside a compute call; the
 // one per-device object it owns is a status word in a __device__ variable.
+#include <math.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -760,6 +762,320 @@ qmoe_status moe_prefill_qgemm(const qmoe_moe_layer *L, const uint16_t *x, int32_
     const int tc_min = g_prefill_tc_min.load();
     a.tc_min = (tc_min > 0 && prefill_tc_supported(a.H, a.I)) ? tc_min : (1 << 30);
     return cuda_status(launch_prefill(a, launch_cfg(d, stream)));
+}
+
+// ------------------------------------------- attention and what feeds it
+qmoe_status rope_frequencies(int32_t rot_dim, double base, int32_t kind, double factor,
+                             int32_t trained, double low, double high, double *inv_freq,
+                             float *scale)
+{
+    if (!inv_freq || !scale || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || kind < QMOE_ROPE_PLAIN ||
+        kind > QMOE_ROPE_RAMP)
+        return QMOE_ERR_INVALID_ARG;
+    if (kind != QMOE_ROPE_PLAIN && !(factor >= 1.0))
+        return QMOE_ERR_INVALID_ARG;
+    if (kind == QMOE_ROPE_BASE && rot_dim < 4)
+        return QMOE_ERR_INVALID_ARG;
+    if (kind >= QMOE_ROPE_BANDS && (trained < 1 || !(low > 0.0) || !(high > low)))
+        return QMOE_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586;
+    if (kind == QMOE_ROPE_BASE)
+        base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    // RAMP: the pair that turns n times over the trained length, trained
+    // base^(-2i/R) = 2 pi n, at i = R ln(trained / (2 pi n)) / (2 ln base)
+    const int half = rot_dim / 2;
+    double first = 0.0, last = 1.0;
+    if (kind == QMOE_ROPE_RAMP) {
+        first = floor(rot_dim * log(trained / (two_pi * high)) / (2.0 * log(base)));
+        last = ceil(rot_dim * log(trained / (two_pi * low)) / (2.0 * log(base)));
+        first = first < 0.0 ? 0.0 : first;
+        last = last > rot_dim - 1.0 ? rot_dim - 1.0 : last;
+        if (last <= first)
+            last = first + 1e-3;
+    }
+    for (int i = 0; i < half; ++i) {
+        const double f = pow(base, -2.0 * i / rot_dim);
+        double keep = 1.0;   // share of the unscaled frequency
+        if (kind == QMOE_ROPE_LINEAR)
+            keep = 0.0;
+        else if (kind == QMOE_ROPE_BANDS)
+            keep = (trained * f / two_pi - low) / (high - low);
+        else if (kind == QMOE_ROPE_RAMP)
+            keep = 1.0 - (i - first) / (last - first);
+        keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+        inv_freq[i] = kind == QMOE_ROPE_PLAIN || kind == QMOE_ROPE_BASE ? f : f * keep + f / factor * (1.0 - keep);
+    }
+    *scale = kind == QMOE_ROPE_RAMP ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return QMOE_OK;
+}
+
+static qmoe_status check_rope(const qmoe_rope *r, int32_t head_dim)
+{
+    if (!r || !r->inv_freq || r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > head_dim)
+        return QMOE_ERR_INVALID_ARG;
+    if (r->layout != QMOE_ROPE_HALF && r->layout != QMOE_ROPE_INTERLEAVED)
+        return QMOE_ERR_INVALID_ARG;
+    return aligned(r->inv_freq, 8) ? QMOE_OK : QMOE_ERR_ALIGNMENT;
+}
+
+static qmoe_status check_cache(const qmoe_kv_cache *c, const qmoe_kv_batch *b)
+{
+    if (!c || !b || !c->k || !c->v || !b->page_table || !b->q_start || !b->kv_len)
+        return QMOE_ERR_INVALID_ARG;
+    if (c->dtype != QMOE_F16 && c->dtype != QMOE_BF16)
+        return QMOE_ERR_INVALID_ARG;
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->page_stride < 0 ||
+        c->token_stride < 0 || c->head_stride < 0)
+        return QMOE_ERR_INVALID_ARG;
+    if (b->batch < 1 || b->max_pages < 1 || b->tokens < 0 || b->max_new < 0)
+        return QMOE_ERR_INVALID_ARG;
+    // positions are 32-bit numbers
+    if ((long long)b->max_pages * c->page_size > (1ll << 30) || b->tokens > (1 << 28) || b->batch > (1 << 24))
+        return QMOE_ERR_UNSUPPORTED;
+    if (c->head_dim % 8 || c->head_dim > 256)
+        return QMOE_ERR_UNSUPPORTED;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || c->page_stride % 8 || c->token_stride % 8 ||
+        c->head_stride % 8 || !aligned(b->page_table, 4) || !aligned(b->q_start, 4) || !aligned(b->kv_len, 4))
+        return QMOE_ERR_ALIGNMENT;
+    return QMOE_OK;
+}
+
+qmoe_status rope_rotate(const qmoe_rope *rope, const void *x, int64_t x_token_stride,
+                        int64_t x_head_stride, int32_t dtype, int32_t tokens, int32_t heads,
+                        int32_t head_dim, const int32_t *positions, void *out,
+                        int64_t out_token_stride, int64_t out_head_stride, int32_t *status_dev,
+                        void *stream)
+{
+    if (!x || !out || !positions || tokens < 0 || heads < 1 || head_dim < 2 ||
+        (dtype != QMOE_F16 && dtype != QMOE_BF16))
+        return QMOE_ERR_INVALID_ARG;
+    qmoe_status s = check_rope(rope, head_dim);
+    if (s != QMOE_OK)
+        return s;
+    if (head_dim > 1024 || heads > (1 << 20) || tokens > (1 << 28))
+        return QMOE_ERR_UNSUPPORTED;
+    if (!aligned(x, 2) || !aligned(out, 2) || !aligned(positions, 4) || (status_dev && !aligned(status_dev, 4)))
+        return QMOE_ERR_ALIGNMENT;
+    DevState *d;
+    if ((s = device_state(&d)) != QMOE_OK)
+        return s;
+    if (tokens == 0)
+        return QMOE_OK;
+    RopeArgs a = {};
+    a.q = static_cast<const uint16_t *>(x);
+    a.q_out = static_cast<uint16_t *>(out);
+    a.q_token = x_token_stride;
+    a.q_head = x_head_stride;
+    a.qo_token = out_token_stride;
+    a.qo_head = out_head_stride;
+    a.inv_freq = rope->inv_freq;
+    a.positions = positions;
+    a.tokens = tokens;
+    a.heads = heads;
+    a.dim = head_dim;
+    a.rot = rope->rot_dim;
+    a.interleaved = rope->layout == QMOE_ROPE_INTERLEAVED;
+    a.scale = rope->scale;
+    a.status = status_dev ? status_dev : d->status;
+    return cuda_status(launch_rope(a, dtype == QMOE_BF16, launch_cfg(d, stream)));
+}
+
+qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
+                      const qmoe_rope *rope, const int32_t *positions, const qmoe_rows *q,
+                      const qmoe_rows *q_out, int32_t heads, const qmoe_rows *k,
+                      const qmoe_rows *v, int32_t *status_dev, void *stream)
+{
+    qmoe_status s = check_cache(cache, batch);
+    if (s != QMOE_OK)
+        return s;
+    if (!k || !v || !k->data || !v->data)
+        return QMOE_ERR_INVALID_ARG;
+    if (q ? (!rope || !q_out || !q->data || !q_out->data || heads < 1) : (q_out || heads != 0))
+        return QMOE_ERR_INVALID_ARG;
+    if (rope && (s = check_rope(rope, cache->head_dim)) != QMOE_OK)
+        return s;
+    if (heads > (1 << 20) || cache->kv_heads > (1 << 20))
+        return QMOE_ERR_UNSUPPORTED;
+    if (!aligned(k->data, 2) || !aligned(v->data, 2) || (q && (!aligned(q->data, 2) || !aligned(q_out->data, 2))) ||
+        (positions && !aligned(positions, 4)) || (status_dev && !aligned(status_dev, 4)))
+        return QMOE_ERR_ALIGNMENT;
+    DevState *d;
+    if ((s = device_state(&d)) != QMOE_OK)
+        return s;
+    if (batch->tokens == 0)
+        return QMOE_OK;
+    RopeArgs a = {};
+    if (q) {
+        a.q = static_cast<const uint16_t *>(q->data);
+        a.q_token = q->token_stride;
+        a.q_head = q->head_stride;
+        a.q_out = static_cast<uint16_t *>(q_out->data);
+        a.qo_token = q_out->token_stride;
+        a.qo_head = q_out->head_stride;
+    }
+    a.k = static_cast<const uint16_t *>(k->data);
+    a.k_token = k->token_stride;
+    a.k_head = k->head_stride;
+    a.v = static_cast<const uint16_t *>(v->data);
+    a.v_token = v->token_stride;
+    a.v_head = v->head_stride;
+    a.ck = static_cast<uint16_t *>(cache->k);
+    a.cv = static_cast<uint16_t *>(cache->v);
+    a.page_stride = cache->page_stride;
+    a.token_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.dim = cache->head_dim;
+    a.table = batch->page_table;
+    a.q_start = batch->q_start;
+    a.kv_len = batch->kv_len;
+    a.batch = batch->batch;
+    a.max_pages = batch->max_pages;
+    a.tokens = batch->tokens;
+    a.heads = heads;
+    a.positions = positions;
+    if (rope) {
+        a.inv_freq = rope->inv_freq;
+        a.rot = rope->rot_dim;
+        a.interleaved = rope->layout == QMOE_ROPE_INTERLEAVED;
+        a.scale = rope->scale;
+    }
+    a.status = status_dev ? status_dev : d->status;
+    return cuda_status(launch_rope(a, cache->dtype == QMOE_BF16, launch_cfg(d, stream)));
+}
+
+size_t attn_paged_workspace_bytes(int32_t head_dim, int64_t max_rows)
+{
+    if (head_dim < 8 || head_dim > 256 || head_dim % 8 || max_rows < 1)
+        return 0;
+    return attn_workspace_bytes(head_dim, max_rows);
+}
+
+qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
+                       const qmoe_kv_batch *batch, void *workspace, size_t workspace_bytes,
+                       int32_t *status_dev, void *stream)
+{
+    if (!attn || !attn->q.data || !attn->out.data)
+        return QMOE_ERR_INVALID_ARG;
+    qmoe_status s = check_cache(cache, batch);
+    if (s != QMOE_OK)
+        return s;
+    if (attn->heads < 1 || attn->heads % cache->kv_heads || attn->window < 0 || !(attn->softcap >= 0.f) ||
+        !(attn->scale > 0.f))
+        return QMOE_ERR_INVALID_ARG;
+    const int group = attn->heads / cache->kv_heads;
+    if ((long long)batch->tokens * group > (1ll << 30) || (long long)batch->tokens * attn->heads > (1ll << 31))
+        return QMOE_ERR_UNSUPPORTED;
+    if (!aligned(attn->q.data, 16) || !aligned(attn->out.data, 16) || attn->q.token_stride % 8 ||
+        attn->q.head_stride % 8 || attn->out.token_stride % 8 || attn->out.head_stride % 8 ||
+        (attn->lse && !aligned(attn->lse, 4)) || (status_dev && !aligned(status_dev, 4)))
+        return QMOE_ERR_ALIGNMENT;
+    long long max_rows = (long long)(batch->max_new ? batch->max_new : batch->tokens) * group;
+    max_rows = max_rows < 1 ? 1 : max_rows;
+    if (!workspace || workspace_bytes < attn_workspace_bytes(cache->head_dim, max_rows))
+        return QMOE_ERR_WORKSPACE;
+    if (!aligned(workspace, 16))
+        return QMOE_ERR_ALIGNMENT;
+    DevState *d;
+    if ((s = device_state(&d)) != QMOE_OK)
+        return s;
+    if (batch->tokens == 0)
+        return QMOE_OK;
+    AttnArgs a = {};
+    a.q = static_cast<const uint16_t *>(attn->q.data);
+    a.q_token = attn->q.token_stride;
+    a.q_head = attn->q.head_stride;
+    a.out = static_cast<uint16_t *>(attn->out.data);
+    a.o_token = attn->out.token_stride;
+    a.o_head = attn->out.head_stride;
+    a.lse = attn->lse;
+    a.k = static_cast<const uint16_t *>(cache->k);
+    a.v = static_cast<const uint16_t *>(cache->v);
+    a.page_stride = cache->page_stride;
+    a.token_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.num_pages = cache->num_pages;
+    a.page_size = cache->page_size;
+    a.kv_heads = cache->kv_heads;
+    a.dim = cache->head_dim;
+    a.table = batch->page_table;
+    a.q_start = batch->q_start;
+    a.kv_len = batch->kv_len;
+    a.batch = batch->batch;
+    a.max_pages = batch->max_pages;
+    a.tokens = batch->tokens;
+    a.heads = attn->heads;
+    a.group = group;
+    a.scale = attn->scale;
+    a.softcap = attn->softcap;
+    a.window = attn->window;
+    a.causal = attn->causal != 0;
+    a.ctr = static_cast<int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAttnCounterBytes);
+    a.status = status_dev ? status_dev : d->status;
+    return cuda_status(launch_attn(a, cache->dtype == QMOE_BF16, max_rows, launch_cfg(d, stream)));
+}
+
+qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, int64_t in_stride,
+                           int32_t dtype, int32_t rows, int32_t vocab, void *out,
+                           int64_t out_stride, int32_t *status_dev, void *stream)
+{
+    if (!rules || !logits || !out || rows < 0 || vocab < 1 || in_stride < 0 || out_stride < 0 ||
+        dtype < QMOE_F16 || dtype > QMOE_F32)
+        return QMOE_ERR_INVALID_ARG;
+    if (rules->history ? (!rules->history_len || rules->max_history < 0 || rules->history_stride < 0)
+                       : rules->max_history != 0)
+        return QMOE_ERR_INVALID_ARG;
+    if (!rules->history && (rules->repetition || rules->presence || rules->frequency))
+        return QMOE_ERR_INVALID_ARG;
+    if (rules->max_bias < 0 || (rules->max_bias > 0 && (!rules->bias_ids || !rules->bias)) ||
+        (rules->mask && rules->mask_stride < 0))
+        return QMOE_ERR_INVALID_ARG;
+    // rows may follow each other closely but not lie inside each other
+    if (rows > 1 && (out_stride < vocab || in_stride < vocab ||
+                     (rules->mask && rules->mask_stride && rules->mask_stride < (vocab + 31) / 32) ||
+                     (rules->history && rules->history_stride < rules->max_history)))
+        return QMOE_ERR_INVALID_ARG;
+    if (rows > 65535 || rules->max_history >= (1 << 20) || rules->max_bias > kMaxLogitBias || vocab > (1 << 28))
+        return QMOE_ERR_UNSUPPORTED;
+    const size_t es = dtype == QMOE_F32 ? 4 : 2;
+    const void *words[] = {rules->history, rules->history_len, rules->prompt_len, rules->repetition,
+                           rules->presence, rules->frequency, rules->bias_ids, rules->bias, rules->mask, status_dev};
+    for (const void *p : words)
+        if (!aligned(p, 4))
+            return QMOE_ERR_ALIGNMENT;
+    if (!aligned(logits, es) || !aligned(out, es))
+        return QMOE_ERR_ALIGNMENT;
+    qmoe_status s;
+    DevState *d;
+    if ((s = device_state(&d)) != QMOE_OK)
+        return s;
+    if (rows == 0)
+        return QMOE_OK;
+    LogitsArgs a = {};
+    a.in = logits;
+    a.out = out;
+    a.in_stride = in_stride;
+    a.out_stride = out_stride;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.history = rules->history;
+    a.history_len = rules->history_len;
+    a.prompt_len = rules->prompt_len;
+    a.history_stride = rules->history_stride;
+    a.max_history = rules->max_history;
+    a.repetition = rules->repetition;
+    a.presence = rules->presence;
+    a.frequency = rules->frequency;
+    a.bias_ids = rules->bias_ids;
+    a.bias = rules->bias;
+    a.max_bias = rules->max_bias;
+    a.mask = rules->mask;
+    a.mask_stride = rules->mask_stride;
+    a.status = status_dev ? status_dev : d->status;
+    return cuda_status(launch_logits(a, dtype, launch_cfg(d, stream)));
 }
 
 qmoe_status qmoe_pack_codes(const uint8_t *codes, int32_t rows, int32_t cols, int32_t bits,

@@ -1,0 +1,373 @@
+// attn.cuh -- what the attention kernels share: the division of the work over
+// the CTAs, the rows' visible keys, and the joining of a unit that several
+// CTAs worked on.
+//
+// A unit is (sequence, block of M query rows, K/V head).  The rows of a unit
+// are (token, query head of the K/V head's group) pairs, token-major, so that
+// one K/V tile in shared memory serves every query head that reads it.  The
+// unit's keys are walked in tiles of KT.  All tiles of all units form one
+// line, cut into equal intervals, one per CTA: a batch of ragged
+// lengths keeps every SM busy to the end, one long context spreads over the
+// whole GPU, and nothing about the lengths is needed on the host (a captured
+// graph replays with new ones).  A unit that crosses CTA borders is finished
+// by its last CTA to arrive, which adds the fp32 partial results in tile
+// order; nobody waits, and results do not depend on the order of arrival.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace qmoe {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <class T>
+struct Num16;
+template <>
+struct Num16<__half> {
+    static __device__ __forceinline__ float up(uint16_t v) { return __half2float(__ushort_as_half(v)); }
+    static __device__ __forceinline__ uint16_t down(float v) { return __half_as_ushort(__float2half_rn(v)); }
+    static __device__ __forceinline__ uint32_t down2(float lo, float hi)
+    {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 up2(uint32_t v)
+    {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    static constexpr uint32_t kExp = 0x7C007C00u;   // exponent bits of a pair
+};
+template <>
+struct Num16<__nv_bfloat16> {
+    static __device__ __forceinline__ float up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+    static __device__ __forceinline__ uint16_t down(float v)
+    {
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+    static __device__ __forceinline__ uint32_t down2(float lo, float hi)
+    {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 up2(uint32_t v)
+    {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    static constexpr uint32_t kExp = 0x7F807F80u;
+};
+
+// whether one of the two 16-bit numbers of a word is an infinity or a NaN
+template <class T>
+__device__ __forceinline__ bool nonfinite2(uint32_t w)
+{
+    const uint32_t e = w & Num16<T>::kExp;
+    return (e & 0xFFFFu) == (Num16<T>::kExp & 0xFFFFu) || (e >> 16) == (Num16<T>::kExp >> 16);
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap * tanh(x / cap) from tanh(z) = 1 - 2 / (1 + e^2z): one exponential and
+// one reciprocal, absolute error a few 2^-23 of cap (the hardware's tanh is
+// good to 2^-11 of cap only, which would show in the weights).  c2 = 2 log2(e)
+// / cap; cap_out may carry another factor along.
+__device__ __forceinline__ float capped(float x, float c2, float cap_out)
+{
+    return cap_out * (1.f - __fdividef(2.f, 1.f + exp2_approx(x * c2)));
+}
+
+// ------------------------------------------------------------------- units --
+struct AttnSeq {
+    int q0, n, len;   // first query row, new tokens, cached tokens with them
+};
+
+// Lengths as the device finds them, kept inside the buffers: a length beyond
+// the page table is cut there and flagged.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs &a, int b)
+{
+    AttnSeq s;
+    s.q0 = min(max(a.q_start[b], 0), a.tokens);
+    s.n = min(max(a.q_start[b + 1], s.q0), a.tokens) - s.q0;
+    const long long room = (long long)a.max_pages * a.page_size;
+    const int len = max(a.kv_len[b], 0);
+    s.len = (long long)len > room ? (int)room : len;
+    return s;
+}
+
+// keys of one token: [lo, hi)
+__device__ __forceinline__ void attn_keys(const AttnArgs &a, const AttnSeq &s, int token, int &lo, int &hi)
+{
+    const int p = s.len - s.n + token;
+    hi = a.causal ? max(p + 1, 0) : s.len;
+    lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+}
+
+// first tile and number of tiles of row block rt (at least one, so that rows
+// that see nothing are written too), and the keys any of its rows sees
+template <int M, int KT>
+__device__ __forceinline__ void attn_tiles(const AttnArgs &a, const AttnSeq &s, int rt, int &t0, int &nt,
+                                           int &lo, int &hi)
+{
+    const int rows = s.n * a.group;
+    int d;
+    attn_keys(a, s, rt * M / a.group, lo, d);
+    attn_keys(a, s, (min(rt * M + M, rows) - 1) / a.group, d, hi);
+    if (hi <= lo) {   // nothing visible
+        t0 = lo = hi = 0;
+        nt = 1;
+        return;
+    }
+    t0 = lo / KT;
+    nt = (hi + KT - 1) / KT - t0;
+}
+
+template <int M>
+__device__ __forceinline__ int attn_blocks(const AttnArgs &a, const AttnSeq &s)
+{
+    return (int)(((long long)s.n * a.group + M - 1) / M);
+}
+
+template <int M, int KT>
+__device__ __forceinline__ long long attn_seq_tiles(const AttnArgs &a, const AttnSeq &s)
+{
+    long long w = 0;
+    const int nb = attn_blocks<M>(a, s);
+    for (int rt = 0; rt < nb; ++rt) {
+        int t0, nt, lo, hi;
+        attn_tiles<M, KT>(a, s, rt, t0, nt, lo, hi);
+        w += nt;
+    }
+    return w * a.kv_heads;
+}
+
+// Inclusive sum of v over the first NT threads' lanes; sm: NT/32 words.
+template <int NT>
+__device__ __forceinline__ long long block_scan(long long v, long long *sm, long long &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o)
+            v += u;
+    }
+    if (lane == 31)
+        sm[warp] = v;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp)
+            before += sm[w];
+        total += sm[w];
+    }
+    __syncthreads();
+    return v + before;
+}
+
+// This CTA's interval [x, end) of the line of tiles, and the sequence that
+// holds tile x with the line's index of its first tile.
+struct AttnSpan {
+    long long total, x, end, first;
+    int b;
+    int ctas;   // CTAs with work: each has at least one tile
+};
+
+// all NT threads of the CTA; sm: NT/32 + 2 words of shared memory
+template <int M, int KT, int NT>
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, long long *sm)
+{
+    AttnSpan sp;
+    long long total = 0, mine = 0, incl = 0, sum;
+    for (int b0 = 0; b0 < a.batch; b0 += NT) {
+        const int b = b0 + (int)threadIdx.x;
+        mine = b < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b)) : 0;
+        if (blockIdx.x == 0 && b < a.batch && a.kv_len[b] > (long long)a.max_pages * a.page_size)
+            flag_status(a.status, QMOE_DEV_BAD_PAGE);
+        incl = block_scan<NT>(mine, sm, sum);
+        total += sum;
+    }
+    sp.total = total;
+    sp.ctas = (int)min(total, (long long)gridDim.x);
+    const long long c = min((int)blockIdx.x, sp.ctas);
+    sp.x = sp.ctas ? total * c / sp.ctas : 0;
+    sp.end = c < sp.ctas ? total * (c + 1) / sp.ctas : sp.x;
+    if (sp.x >= sp.end)
+        return sp;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += NT) {
+        if (a.batch > NT) {
+            const int b = b0 + (int)threadIdx.x;
+            mine = b < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b)) : 0;
+            incl = block_scan<NT>(mine, sm, sum);
+        } else {
+            sum = total;
+        }
+        if (before + incl - mine <= sp.x && sp.x < before + incl) {
+            sm[NT / 32] = before + incl - mine;
+            sm[NT / 32 + 1] = b0 + (int)threadIdx.x;
+        }
+        before += sum;
+        if (before > sp.x)
+            break;
+    }
+    __syncthreads();
+    sp.first = sm[NT / 32];
+    sp.b = (int)sm[NT / 32 + 1];
+    return sp;
+}
+
+// the CTA that works on tile x of the line
+__device__ __forceinline__ int attn_cta(const AttnSpan &sp, long long x)
+{
+    return (int)(((x + 1) * sp.ctas - 1) / sp.total);
+}
+
+// A walk over the units of a CTA's interval.
+template <int M, int KT>
+struct AttnWalk {
+    AttnSpan sp;
+    AttnSeq s;
+    int rt, nb, h;           // row block (of nb), K/V head
+    int t0, nt, lo, hi;      // tiles and keys of the row block
+    long long u0;            // line index of the unit's first tile
+
+    __device__ __forceinline__ void start(const AttnArgs &a, const AttnSpan &span)
+    {
+        sp = span;
+        if (sp.x >= sp.end)
+            return;
+        s = attn_seq(a, sp.b);
+        nb = attn_blocks<M>(a, s);
+        u0 = sp.first;
+        for (rt = 0;; ++rt) {
+            attn_tiles<M, KT>(a, s, rt, t0, nt, lo, hi);
+            if (sp.x < u0 + (long long)nt * a.kv_heads || rt + 1 >= nb)
+                break;
+            u0 += (long long)nt * a.kv_heads;
+        }
+        h = (int)((sp.x - u0) / nt);
+        u0 += (long long)h * nt;
+    }
+    __device__ __forceinline__ bool done() const { return sp.x >= sp.end; }
+    // the unit's tiles that are this CTA's: [ta, tb) of 0..nt
+    __device__ __forceinline__ int ta() const { return (int)(sp.x - u0); }
+    __device__ __forceinline__ int tb() const { return (int)(min(sp.end, u0 + nt) - u0); }
+    __device__ __forceinline__ void next(const AttnArgs &a)
+    {
+        u0 += nt;
+        sp.x = u0;
+        if (done())
+            return;
+        if (++h < a.kv_heads)
+            return;
+        h = 0;
+        ++rt;
+        while (rt >= nb) {   // sp.x < sp.end <= total: a later sequence has tiles
+            s = attn_seq(a, ++sp.b);
+            nb = attn_blocks<M>(a, s);
+            rt = 0;
+        }
+        attn_tiles<M, KT>(a, s, rt, t0, nt, lo, hi);
+    }
+};
+
+// Where the first element of cached token j of sequence b (K/V head h) lies,
+// or -1 for a page id outside the cache (flagged by the caller).
+__device__ __forceinline__ long long attn_slot(const AttnArgs &a, int b, int h, int j)
+{
+    const int pg = (int)((unsigned)j / (unsigned)a.page_size);
+    const int id = __ldg(a.table + (size_t)b * a.max_pages + pg);
+    if ((unsigned)id >= (unsigned)a.num_pages)
+        return -1;
+    return id * a.page_stride + (long long)(j - pg * a.page_size) * a.token_stride + h * a.head_stride;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ----------------------------------------------------------------- joining --
+// Partial results of CTA c: two slots of M rows x DP fp32 sums, then M maxima
+// (log2 units) and M weight sums.  Slot 0 holds the part of a unit that began
+// in an earlier CTA, slot 1 of one that goes on in a later one.
+template <int M, int DP>
+__device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, int slot)
+{
+    return a.part + (size_t)(2 * cta + slot) * M * (DP + 2);
+}
+
+// Announces this CTA's part of a unit that CTAs c0..c1 share; true for the
+// last one, which then reads all parts.  All NT threads of the CTA.
+template <int NT>
+__device__ __forceinline__ bool attn_arrive(const AttnArgs &a, int c0, int c1, int *sm)
+{
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const int got = atomicAdd(a.ctr + c0, 1);
+        *sm = got == c1 - c0;
+        if (got == c1 - c0)
+            a.ctr[c0] = 0;
+        __threadfence();
+    }
+    __syncthreads();
+    return *sm != 0;
+}
+
+// out / lse of one unit row from its parts c0..c1, 4 columns a thread
+template <class T, int M, int DP, int NT>
+__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnSeq &s, int rt, int h, int c0, int c1)
+{
+    const int rows = min(M, s.n * a.group - rt * M);
+    const int d4 = a.dim / 4;
+    const int nseg = c1 - c0 + 1;
+    for (int i = threadIdx.x; i < rows * d4; i += NT) {
+        const int r = i / d4, d = (i - r * d4) * 4;
+        float m = -INFINITY;
+        for (int k = 0; k < nseg; ++k)
+            m = fmaxf(m, __ldcg(attn_part<M, DP>(a, c0 + k, k == 0) + M * DP + r));
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < nseg; ++k) {
+            const float *p = attn_part<M, DP>(a, c0 + k, k == 0);
+            const float w = exp2_approx(__ldcg(p + M * DP + r) - base);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)r * DP + d));
+            l = fmaf(w, __ldcg(p + M * DP + M + r), l);
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = rt * M + r;
+        const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+        uint2 w2;
+        w2.x = Num16<T>::down2(o.x * inv, o.y * inv);
+        w2.y = Num16<T>::down2(o.z * inv, o.w * inv);
+        *reinterpret_cast<uint2 *>(a.out + (size_t)(s.q0 + tok) * a.o_token + (size_t)hq * a.o_head + d) = w2;
+        if (a.lse && d == 0)
+            a.lse[(size_t)(s.q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+}
+
+}  // namespace qmoe

@@ -229,6 +229,67 @@ constexpr int kTcMinTokens = 16;
 // the shared-memory ring of the grouped kernels holds at least two units
 bool prefill_shape_supported(int hidden, int inter);
 
+// --------------------------------------------- attention over a paged cache --
+struct AttnArgs {
+    const uint16_t *q, *k, *v;       // 16-bit numbers (fp16 or bf16)
+    uint16_t *out;                   // [tokens][heads][dim] by strides
+    float *lse;                      // [tokens][heads] or null
+    const int32_t *table;            // [batch][max_pages]
+    const int32_t *q_start;          // [batch + 1]
+    const int32_t *kv_len;           // [batch]
+    long long q_token, q_head, o_token, o_head;          // strides, elements
+    long long page_stride, token_stride, head_stride;    // of the cache
+    int batch, tokens, heads, kv_heads, group, dim;
+    int page_size, num_pages, max_pages;
+    float scale, softcap;
+    int window, causal;
+    float *part;                     // partial results of units that several CTAs share
+    int *ctr;                        // their arrival counters, zero between calls
+    int32_t *status;
+};
+// rows (tokens x query heads of one K/V head) of the longest sequence decide
+// the row block; `bf16` the type
+cudaError_t launch_attn(const AttnArgs &a, bool bf16, long long max_rows, const LaunchCfg &c);
+size_t attn_workspace_bytes(int dim, long long max_rows);
+constexpr int kAttnMaxCtas = 480;            // at most 3 CTAs on each of 160 SMs
+constexpr size_t kAttnCounterBytes = 4096;   // one int32 arrival counter per CTA
+
+// ----------------------------------------------- rotary positions, append --
+struct RopeArgs {
+    const uint16_t *q, *k, *v;       // [tokens][heads][dim] by strides; k, v null: q only
+    uint16_t *q_out, *ck, *cv;       // rotated q; the cache
+    const double *inv_freq;          // [rot / 2] radians per position, null: no rotation
+    const int32_t *positions;        // [tokens], or null: from the cache lengths
+    const int32_t *table, *q_start, *kv_len;
+    long long q_token, q_head, qo_token, qo_head, k_token, k_head, v_token, v_head;
+    long long page_stride, token_stride, head_stride;
+    int batch, tokens, heads, kv_heads, dim, rot, interleaved;
+    int page_size, num_pages, max_pages;
+    float scale;
+    int32_t *status;
+};
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, const LaunchCfg &c);
+
+// ------------------------------------------------------- rules on logits --
+struct LogitsArgs {
+    const void *in;
+    void *out;                       // may be `in`
+    long long in_stride, out_stride; // elements
+    int rows, vocab;
+    const int32_t *history, *history_len, *prompt_len;
+    long long history_stride;
+    int max_history;
+    const float *repetition, *presence, *frequency;   // [rows] or null
+    const int32_t *bias_ids;         // [rows][max_bias], -1: unused
+    const float *bias;
+    int max_bias;
+    const uint32_t *mask;            // [rows] of mask_stride words, or null
+    long long mask_stride;
+    int32_t *status;
+};
+constexpr int kMaxLogitBias = 1024;
+cudaError_t launch_logits(const LogitsArgs &a, int dtype, const LaunchCfg &c);
+
 // ------------------------------------------------------------ pack helpers --
 cudaError_t launch_pack(const uint8_t *codes, int rows, int cols, int bits, uint32_t *packed,
                         cudaStream_t s);

@@ -27,6 +27,8 @@ ERR_TIMEOUT = -6
 ERR_WORKSPACE = -7
 DEV_BAD_EXPERT = 0x1
 DEV_TIMEOUT = 0x2
+DEV_BAD_PAGE = 0x4
+DEV_BAD_TOKEN = 0x8
 
 
 class QmoeError(RuntimeError):
@@ -57,6 +59,7 @@ def lib():
             _build.build()
         L = ctypes.CDLL(path)
         p, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        i64 = ctypes.c_int64
         sig = {
             "qgemv_affine": [p, p, i32, p, p, p],
             "qgemv_affine_workspace_bytes": [i32, i32, i32, i32],
@@ -79,6 +82,13 @@ def lib():
             "moe_decode_layers_host": [p, i32, i32, i32, i32, p, p, i32, p, p, p, sz, p, p],
             "moe_prefill_workspace_bytes": [p, i32, i32],
             "moe_prefill_qgemm": [p, p, i32, p, p, i32, p, p, sz, p, p],
+            "rope_frequencies": [i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double,
+                                 ctypes.c_double, p, p],
+            "rope_rotate": [p, p, i64, i64, i32, i32, i32, i32, p, p, i64, i64, p, p],
+            "kv_append": [p, p, p, p, p, p, i32, p, p, p, p],
+            "attn_paged_workspace_bytes": [i32, i64],
+            "attn_paged": [p, p, p, p, sz, p, p],
+            "logits_process": [p, p, i64, i32, i32, i32, p, i64, p, p],
             "qmoe_pack_codes": [p, i32, i32, i32, p, p],
             "qmoe_unpack_codes": [p, i32, i32, i32, p, p],
             "qmoe_check_status": [p, p, p],
@@ -106,6 +116,7 @@ def lib():
         L.moe_prefill_workspace_bytes.restype = sz
         L.moe_decode_workspace_bytes.restype = sz
         L.moe_decode_pack_bytes.restype = sz
+        L.attn_paged_workspace_bytes.restype = sz
         L.qmoe_status_string.restype = ctypes.c_char_p
         L.qmoe_version.restype = i32
         L.qmoe_set_dependent_launch.restype = i32
@@ -640,6 +651,338 @@ def moe_prefill_qgemm(layer, x, idx, weights, y=None, workspace=None, status=Non
                                    top_k, _ptr(y), _ptr(workspace), workspace.numel(),
                                    _ptr(status), _stream()), "moe_prefill_qgemm")
     return y
+
+
+# ------------------------------------- positions, paged cache, attention --
+class CKVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class CKVBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("max_new", ctypes.c_int32)]
+
+
+class CRope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class CAttn(ctypes.Structure):
+    _fields_ = [("q", CRows), ("out", CRows), ("lse", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float)]
+
+
+class CLogitRules(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("history_stride", ctypes.c_int64),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64), ("max_history", ctypes.c_int32),
+                ("max_bias", ctypes.c_int32)]
+
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+
+def _device_call(fn, what, device, *args):
+    """fn(*args, current stream of `device`) with `device` current."""
+    if device.index == torch.cuda.current_device():
+        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if code != OK:
+        raise QmoeError(code, what)
+
+
+def _on(device, t, what):
+    if t.device != device:
+        raise ValueError("%s is on %s, the other tensors on %s" % (what, t.device, device))
+    return t
+
+
+def _opt(t, dtype, what, shape, device):
+    """Address of an optional contiguous tensor (None: 0)."""
+    if t is None:
+        return None
+    return _on(device, _need(t, dtype, what, shape), what).data_ptr()
+
+
+def _rows(t, what, dtype, device, shape):
+    """A [tokens][heads][dim] tensor of any token and head strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+        raise TypeError("%s must be a %s tensor on %s" % (what, dtype, device))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError("%s: the elements of a head must follow each other" % what)
+    # the stride of a dimension of one element says nothing
+    return CRows(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+
+
+class KVCache:
+    """One layer's paged K/V cache: k, v float16 or bfloat16 [num_pages]
+    [page_size][kv_heads][head_dim], both with the same strides (a transposed
+    view of [num_pages][kv_heads][page_size][head_dim] tensors is as good)."""
+
+    def __init__(self, k, v):
+        for t, what in ((k, "k"), (v, "v")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+                raise TypeError("%s must be a CUDA tensor [pages][page size][heads][dim]" % what)
+            if t.dtype not in (torch.float16, torch.bfloat16):
+                raise TypeError("%s must be float16 or bfloat16" % what)
+        if k.dtype != v.dtype or k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must agree in type, shape, strides and device")
+        if k.stride(3) != 1:
+            raise ValueError("the elements of a head must follow each other")
+        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        strides = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
+        self.c = CKVCache(k.data_ptr(), v.data_ptr(), *strides, *k.shape, _DTYPES[k.dtype])
+        self._ref = ctypes.addressof(self.c)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype=torch.float16, device="cuda"):
+        n = (num_pages, page_size, kv_heads, head_dim)
+        return cls(torch.empty(n, dtype=dtype, device=device), torch.empty(n, dtype=dtype, device=device))
+
+
+class KVBatch:
+    """A step's sequences: page_table int32 [B][max_pages], q_start int32
+    [B + 1] (sequence b's new tokens are rows q_start[b] .. q_start[b+1]),
+    kv_len int32 [B] (cached tokens with the new ones).  max_new: an upper
+    bound of the new tokens per sequence, which chooses the kernel."""
+
+    def __init__(self, page_table, q_start, kv_len, max_new=0):
+        _need(page_table, torch.int32, "page_table")
+        if page_table.dim() != 2 or page_table.numel() == 0:
+            raise ValueError("page_table must be [batch][pages], not empty")
+        B = page_table.shape[0]
+        _need(q_start, torch.int32, "q_start", (B + 1,))
+        _need(kv_len, torch.int32, "kv_len", (B,))
+        self.device = page_table.device
+        _on(self.device, q_start, "q_start")
+        _on(self.device, kv_len, "kv_len")
+        self.page_table, self.q_start, self.kv_len, self.max_new = page_table, q_start, kv_len, int(max_new)
+        self._by_tokens = {}
+
+    def _c(self, tokens):
+        """Address of the C struct for steps of `tokens` rows."""
+        c = self._by_tokens.get(tokens)
+        if c is None:
+            c = CKVBatch(self.page_table.data_ptr(), self.q_start.data_ptr(), self.kv_len.data_ptr(),
+                         self.page_table.shape[0], self.page_table.shape[1], tokens, self.max_new)
+            self._by_tokens[tokens] = c
+        return ctypes.addressof(c)
+
+
+def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, trained=0, low=1.0, high=4.0):
+    """(float64 [rot_dim / 2] CPU tensor of radians per position, scale)."""
+    f = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    scale = ctypes.c_float()
+    _check(lib().rope_frequencies(rot_dim, base, ROPE_KINDS[kind], factor, trained, low, high,
+                                  f.data_ptr(), ctypes.addressof(scale)), "rope_frequencies")
+    return f, scale.value
+
+
+class Rope:
+    """Rotary positions: inv_freq float64 [rot_dim / 2] on the GPU, layout
+    "half" or "interleaved", scale of the turned part."""
+
+    def __init__(self, inv_freq, layout="half", scale=1.0):
+        _need(inv_freq, torch.float64, "inv_freq")
+        if inv_freq.dim() != 1 or inv_freq.numel() == 0:
+            raise ValueError("inv_freq must be [rot_dim / 2]")
+        self.inv_freq, self.device, self.rot_dim = inv_freq, inv_freq.device, 2 * inv_freq.numel()
+        self.c = CRope(inv_freq.data_ptr(), self.rot_dim, ROPE_LAYOUTS[layout], scale)
+        self._ref = ctypes.addressof(self.c)
+
+    @classmethod
+    def make(cls, rot_dim, layout="half", device="cuda", **kw):
+        """With the frequencies of rope_frequencies(rot_dim, **kw)."""
+        f, scale = rope_frequencies(rot_dim, **kw)
+        return cls(f.to(device), layout, scale)
+
+
+def rope_rotate(rope, x, positions, out=None, status=None):
+    """x [T][H][D] float16 or bfloat16 turned to `positions` int32 [T]."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("x must be a float16 or bfloat16 tensor [tokens][heads][dim]")
+    dev = _on(rope.device, x, "x").device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    cx, co = _rows(x, "x", x.dtype, dev, x.shape), _rows(out, "out", x.dtype, dev, x.shape)
+    T, H, D = x.shape
+    if x.numel() == 0:   # empty tensors have no address
+        return out
+    _device_call(lib().rope_rotate, "rope_rotate", dev, rope._ref, cx.data, cx.token_stride, cx.head_stride,
+                 _DTYPES[x.dtype], T, H, D, _opt(positions, torch.int32, "positions", (T,), dev), co.data,
+                 co.token_stride, co.head_stride, _ptr(status))
+    return out
+
+
+def kv_append(cache, batch, k, v, q=None, rope=None, positions=None, q_out=None, status=None):
+    """Store a step's keys (turned by `rope`) and values [T][kv_heads][D] in
+    the cache and return the step's queries q [T][heads][D] turned likewise
+    (None without q), in one launch.  positions int32 [T]: the rotation's
+    positions where they are not the rows' places in their sequences."""
+    dev, dt = cache.device, cache.dtype
+    if batch.device != dev or (rope is not None and rope.device != dev):
+        raise ValueError("cache, batch and rope must be on one device")
+    T = k.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    ck, cv = _rows(k, "k", dt, dev, shape), _rows(v, "v", dt, dev, shape)
+    cq = co = None
+    heads = 0
+    if q is not None:
+        if rope is None:
+            raise ValueError("q needs rope")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+        heads = q.shape[1]
+        shape = (T, heads, cache.head_dim)
+        cq = ctypes.byref(_rows(q, "q", dt, dev, shape))
+        co = ctypes.byref(_rows(q_out, "q_out", dt, dev, shape))
+    if T == 0:   # empty tensors have no address
+        return q_out
+    _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T), rope._ref if rope else None,
+                 _opt(positions, torch.int32, "positions", (T,), dev), cq, co, heads, ctypes.byref(ck),
+                 ctypes.byref(cv), _ptr(status))
+    return q_out
+
+
+_ATTN_COUNTER_BYTES = 4096   # the part of a workspace that has to start as zeros
+_attn_ws = {}
+
+
+def attn_workspace(head_dim, max_rows, device="cuda"):
+    """A workspace for attn_paged calls of at most max_rows = new tokens x
+    query heads per K/V head rows in a sequence."""
+    need = lib().attn_paged_workspace_bytes(head_dim, max_rows)
+    if not need:
+        raise ValueError("unsupported head_dim %d" % head_dim)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws[:_ATTN_COUNTER_BYTES].zero_()
+    return ws
+
+
+def _attn_workspace(head_dim, max_rows, device, stream):
+    """One workspace for each stream; in a capture one of the graph's own (its
+    zeros are set by the graph)."""
+    if torch.cuda.is_current_stream_capturing():
+        return attn_workspace(head_dim, max_rows, device)
+    need = lib().attn_paged_workspace_bytes(head_dim, max_rows)
+    ws = _attn_ws.get((device.index, stream))
+    if ws is None or ws.numel() < need:
+        ws = _attn_ws[(device.index, stream)] = attn_workspace(head_dim, max_rows, device)
+    return ws
+
+
+def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, softcap=0.0, window=0,
+               causal=True, workspace=None, status=None):
+    """Attention of the step's queries q [T][heads][D] over the cache, which
+    already holds the step's own keys and values.  scale: 1/sqrt(D) unless
+    given; softcap > 0 caps the scores by a tanh; window > 0: a sliding window
+    of that many keys.  Returns out [T][heads][D], or (out, lse float32
+    [T][heads]) with want_lse or lse."""
+    dev = cache.device
+    if batch.device != dev:
+        raise ValueError("cache and batch must be on one device")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q must be a tensor [tokens][heads][dim]")
+    T, H, D = q.shape
+    shape = (T, H, cache.head_dim)
+    cq = _rows(q, "q", cache.dtype, dev, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=cache.dtype, device=dev)
+        co = CRows(out.data_ptr(), H * D, D)
+    else:
+        co = _rows(out, "out", cache.dtype, dev, shape)
+    if lse is None and want_lse:
+        lse = torch.empty(T, H, dtype=torch.float32, device=dev)
+    rows = max((batch.max_new or T) * (H // cache.kv_heads), 1)
+    if workspace is None:
+        workspace = _attn_workspace(D, rows, dev, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        _on(dev, workspace, "workspace")
+    c = CAttn(cq, co, _opt(lse, torch.float32, "lse", (T, H), dev), H, window, 1 if causal else 0,
+              D ** -0.5 if scale is None else scale, softcap)
+    if T == 0:   # empty tensors have no address
+        return out if lse is None else (out, lse)
+    _device_call(lib().attn_paged, "attn_paged", dev, ctypes.addressof(c), cache._ref, batch._c(T),
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status))
+    return out if lse is None else (out, lse)
+
+
+# --------------------------------------------------------- rules on logits --
+def logits_process(logits, out=None, history=None, history_len=None, prompt_len=None, repetition=None,
+                   presence=None, frequency=None, bias_ids=None, bias=None, mask=None, status=None):
+    """Penalties, biases and a grammar mask on logits [rows][vocab] (float16,
+    bfloat16 or float32); out may be logits itself.  history int32 [rows][n]
+    with history_len int32 [rows] tokens in use, prompt_len of them the prompt;
+    repetition, presence, frequency float32 [rows]; bias_ids int32 / bias
+    float32 [rows][m] (-1: unused); mask int32 [rows] or [1] x [ceil(vocab /
+    32)], bit v % 32 of word v / 32 set where token v is allowed."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise TypeError("logits must be a CUDA tensor [rows][vocab] of float16, bfloat16 or float32")
+    R, V = logits.shape
+    dev = logits.device
+    if out is None:
+        out = torch.empty(R, V, dtype=logits.dtype, device=dev)
+    if out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError("out must be like logits")
+    _on(dev, out, "out")
+    if V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+        raise ValueError("a row's logits must follow each other")
+    c = CLogitRules()
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != R or history.dtype != torch.int32 or \
+                (history.shape[1] > 1 and history.stride(1) != 1):
+            raise ValueError("history must be int32 [rows][tokens], the tokens of a row one after the other")
+        c.history, c.history_stride, c.max_history = _on(dev, history, "history").data_ptr(), history.stride(0), history.shape[1]
+        if history_len is None:
+            raise ValueError("history needs history_len")
+        c.history_len = _opt(history_len, torch.int32, "history_len", (R,), dev)
+        c.prompt_len = _opt(prompt_len, torch.int32, "prompt_len", (R,), dev)
+    elif any(t is not None for t in (history_len, prompt_len, repetition, presence, frequency)):
+        raise ValueError("penalties need history")
+    c.repetition = _opt(repetition, torch.float32, "repetition", (R,), dev)
+    c.presence = _opt(presence, torch.float32, "presence", (R,), dev)
+    c.frequency = _opt(frequency, torch.float32, "frequency", (R,), dev)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias and bias_ids go together")
+    if bias is not None:
+        c.max_bias = bias.shape[-1]
+        c.bias_ids = _opt(bias_ids, torch.int32, "bias_ids", (R, c.max_bias), dev)
+        c.bias = _opt(bias, torch.float32, "bias", (R, c.max_bias), dev)
+    if mask is not None:
+        _need(mask, torch.int32, "mask")
+        words = (V + 31) // 32
+        if mask.dim() != 2 or mask.shape[0] not in (1, R) or mask.shape[1] < words:
+            raise ValueError("mask must be int32 [rows] or [1] x at least %d words" % words)
+        c.mask, c.mask_stride = _on(dev, mask, "mask").data_ptr(), mask.shape[1] if mask.shape[0] == R else 0
+    if R == 0 or V == 0:   # empty tensors have no address
+        return out
+    _device_call(lib().logits_process, "logits_process", dev, ctypes.addressof(c), logits.data_ptr(),
+                 logits.stride(0), _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0), _ptr(status))
+    return out
 
 
 def qmoe_pack_codes(codes, bits):
