@@ -125,14 +125,25 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
             if (t < tb) {
                 unsigned char *kt = stage + (t % S) * 2 * L::tile;
                 const long long *o = off + (t % S) * AM_KT;
-#pragma unroll 8
-                for (int i = tid; i < AM_KT * CPR; i += AM_THREADS) {
-                    const int r = i / CPR, c = i % CPR;
-                    const long long e = o[r];
-                    const bool live = e >= 0 && c * 8 < a.dim;
-                    const long long src = live ? e + c * 8 : 0;
-                    cp_async16(smem_u32(kt) + sw<DP>(r, c), a.k + src, live);
-                    cp_async16(smem_u32(kt) + L::tile + sw<DP>(r, c), a.v + src, live);
+                // a thread stays in its column; the offsets of its rows are read
+                // before any copy goes out, so that no copy waits for them
+                constexpr int RP = AM_THREADS / CPR, N = AM_KT / RP, B = N < 8 ? N : 8;
+                const int c = tid % CPR;
+                const bool in = c * 8 < a.dim;
+#pragma unroll
+                for (int i0 = 0; i0 < N; i0 += B) {
+                    long long e[B];
+#pragma unroll
+                    for (int i = 0; i < B; ++i)
+                        e[i] = o[tid / CPR + (i0 + i) * RP];
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        const int r = tid / CPR + (i0 + i) * RP;
+                        const bool live = in && e[i] >= 0;
+                        const long long src = live ? e[i] + c * 8 : 0;
+                        cp_async16(smem_u32(kt) + sw<DP>(r, c), a.k + src, live);
+                        cp_async16(smem_u32(kt) + L::tile + sw<DP>(r, c), a.v + src, live);
+                    }
                 }
             }
             cp_async_commit();
@@ -361,7 +372,8 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
             }
         }
         if (!whole && attn_arrive<AM_THREADS>(a, c0, c1, flag))
-            attn_join<T, M, DP, AM_THREADS>(a, w.s, w.rt, w.h, c0, c1);
+            for (int r = warp; r < rows; r += AM_THREADS / 32)
+                attn_join_row<T, M, DP>(a, c0, c1, r, w.s.q0, row0 + r, w.h);
         __syncthreads();   // the ring and the flags are free for the next unit
     }
 }
@@ -393,17 +405,70 @@ cudaError_t launch_dim(const AttnArgs &a, long long max_rows, const LaunchCfg &c
 
 }  // namespace
 
+bool attn_maps(const AttnArgs &a, bool bf16, int kt, AttnMaps *m, int *rows, int *heads_inner)
+{
+    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode fn = []() -> Encode {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<Encode>(p);
+        (void)cudaGetLastError();
+        return nullptr;
+    }();
+    int r = kt;
+    while (r > a.page_size || a.page_size % r)
+        r /= 2;   // kt is a power of two
+    if (!fn || r < 8 || a.dim < 64)
+        return false;
+    // strides in bytes; that of a dimension of one element says nothing
+    cuuint64_t tok = a.page_size > 1 ? 2 * a.token_stride : 2 * a.dim;
+    cuuint64_t head = a.kv_heads > 1 ? 2 * a.head_stride : 2 * a.dim;
+    const bool hi = a.kv_heads > 1 ? head < tok : true;   // heads inside slots
+    if (a.kv_heads == 1)
+        head = 2 * (cuuint64_t)a.dim;
+    const cuuint64_t s0 = hi ? head : tok, s1 = hi ? tok : head;
+    const cuuint64_t last = s1 * (hi ? a.page_size : a.kv_heads);
+    const cuuint64_t s2 = a.num_pages > 1 ? 2 * (cuuint64_t)a.page_stride : last;
+    const cuuint64_t most = (cuuint64_t)1 << 40;
+    if (s0 < 2 * (cuuint64_t)a.dim || s0 % 16 || s1 % s0 || s1 < s0 || s2 % s1 || s2 < s1 || s2 >= most)
+        return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.dim, (cuuint64_t)(hi ? a.kv_heads : a.page_size),
+                                (cuuint64_t)(hi ? a.page_size : a.kv_heads), (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {s0, s1, s2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(hi ? 1 : r), (cuuint32_t)(hi ? r : 1), 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    *rows = r;
+    *heads_inner = hi;
+    for (int i = 0; i < 2; ++i)
+        if (fn(i ? &m->v : &m->k, type, 4, const_cast<uint16_t *>(i ? a.v : a.k), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
 size_t attn_workspace_bytes(int dim, long long max_rows)
 {
     const int dp = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
     const int m = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
-    return kAttnCounterBytes + (size_t)kAttnMaxCtas * 2 * m * (dp + 2) * 4;
+    const size_t row = (size_t)2 * (dp + 2) * 4;   // two slots
+    if (max_rows > 64)
+        return kAttnCounterBytes + kAttnMaxSms * (256 * row + 32);   // and what the units are
+    return kAttnCounterBytes + (size_t)kAttnMaxSms * 3 * m * row;
 }
 
 cudaError_t launch_attn(const AttnArgs &a, bool bf16, long long max_rows, const LaunchCfg &c)
 {
-    if (c.num_sms * 3 > kAttnMaxCtas)
+    if (c.num_sms > kAttnMaxSms)
         return cudaErrorInvalidValue;
+    if (max_rows > 64)
+        // two row tiles per unit once there are units for every SM
+        return launch_attn_tc(a, bf16, (long long)a.tokens * a.group / 256 * a.kv_heads >= c.num_sms ? 2 : 1, c);
     if (a.dim <= 64)
         return bf16 ? launch_dim<__nv_bfloat16, 64>(a, max_rows, c) : launch_dim<__half, 64>(a, max_rows, c);
     if (a.dim <= 128)

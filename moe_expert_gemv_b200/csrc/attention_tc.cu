@@ -1,0 +1,867 @@
+// attention_tc.cu -- new tokens over a paged K/V cache, many query rows per
+// K/V head (prompt chunks, verified drafts), on the 5th-generation tensor
+// cores.  The formula and the division of the work are attn.cuh's.
+//
+// 4 D operations per visible (query, key) pair bound it: the two products on
+// tcgen05.mma, and beside them one exponential per pair -- at D = 128 the
+// exponentials of a 128 x 128 tile (16 a cycle and SM) cost as much time as
+// its two products, so the kernel keeps both busy at once:
+//   S = Q K^T   both operands in shared memory, S in tensor memory (fp32)
+//   softmax     one thread per row: its S row from tensor memory, running
+//               maximum and sum in registers, the weights back to tensor
+//               memory over S in the cache's 16-bit type
+//   O += P V    P from tensor memory, V as it lies in the cache (MN-major),
+//               O in tensor memory
+// NROW = 2 (head_dim <= 128): a unit is 256 query rows, two row tiles with a
+// softmax warpgroup each; while one tile's weights are made, the other's
+// products run.  NROW = 1 (128 rows; head_dim 256, or few rows): the scores
+// of the next key tile are made while the softmax works on this one.
+// O is rescaled only when a row's maximum has grown by more than 2^8 since
+// the last time: until then the weights are at most 2^8 (exact powers of the
+// same base, no rounding is lost), so most tiles touch O in the product only.
+//
+// Roles: softmax warpgroups, one MMA-issuing thread, 3 loader warps.  K and V
+// arrive in the 128-byte-swizzled blocks of 64 columns that both operand
+// descriptors read, by TMA in boxes of up to a page where the cache has a
+// tensor map, else (page sizes that no multiple of 8 divides, heads below 64)
+// by 16-byte cp.async: 27 cycles per warp instruction, which held a 128-key
+// tile of K and V to 5200 cycles where the products need 2048.
+// Every wait is bounded; on a timeout the roles stop, the copies and products
+// in flight finish and the tensor memory is freed.
+#include "attn.cuh"
+
+namespace qmoe {
+namespace {
+
+constexpr float TC_LAZY = 8.f;   // log2 of the growth of a maximum that O is not rescaled for
+
+template <int DP, int NROW>
+struct TcCfg {
+    static constexpr int KT = DP == 256 ? 64 : 128;      // keys per tile
+    static constexpr int M = 128 * NROW;
+    static constexpr int KS = 2, VS = 2;                 // stages; S buffers: also 2, row tiles or tiles in turn
+    static constexpr int tile = KT * DP * 2;
+    static constexpr int SOFT = 128 * NROW;              // softmax threads
+    static constexpr int LOAD = 96;                      // cp.async threads
+    static constexpr int FIX = 64;                       // beside the TMA warp
+    static constexpr int THREADS = SOFT + 128;
+    // tensor memory columns
+    static constexpr int s_col = 0;                      // + 128 per buffer
+    static constexpr int o_col = 256;                    // + DP per row tile
+    static constexpr int q_off = 0;
+    static constexpr int k_off = q_off + M * DP * 2;
+    static constexpr int v_off = k_off + KS * tile;
+    static constexpr int off_off = v_off + VS * tile;    // [2][KT] int64
+    static constexpr int bar_off = off_off + 2 * KT * 8;
+    static constexpr int misc_off = bar_off + 32 * 8;
+    static constexpr int total = misc_off + 256 + 1024;  // + alignment slack
+    static_assert(o_col + NROW * DP <= 512, "tensor memory");
+    static_assert(total <= 227 * 1024, "shared memory");
+};
+
+enum {
+    TB_QF = 0, TB_QE, TB_KF, TB_KE = TB_KF + 2, TB_VF = TB_KE + 2, TB_VE = TB_VF + 2, TB_SF = TB_VE + 2,
+    TB_PF = TB_SF + 2, TB_OF = TB_PF + 2, TB_OE = TB_OF + 2, TB_VX = TB_OE + 2, TB_PV = TB_VX + 2, TB_DRAIN, TB_COUNT
+};
+static_assert(TB_COUNT <= 32, "barriers");
+constexpr int TC_BAR_SOFT = 1, TC_BAR_LOAD = 2;   // named barriers
+
+// 128-byte-swizzled operand blocks of 64 columns (128-byte rows, 8-row groups
+// 1024 bytes apart); lead: bytes between blocks of 64 columns, read for the
+// MN-major operand only
+__device__ __forceinline__ uint64_t at_desc(uint32_t saddr, uint32_t lead)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// fp32 D, M = 128, N = n; A and B both fp16 or both bf16; b_mn: B is MN-major
+template <class T>
+__device__ __forceinline__ uint32_t at_idesc(int n, bool b_mn)
+{
+    const uint32_t f = sizeof(T) == 2 && Num16<T>::kExp == 0x7F807F80u ? 1u : 0u;
+    return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void at_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void at_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void at_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+#define AT_R32(v, o)                                                                                              \
+    v[o], v[o + 1], v[o + 2], v[o + 3], v[o + 4], v[o + 5], v[o + 6], v[o + 7], v[o + 8], v[o + 9], v[o + 10],    \
+        v[o + 11], v[o + 12], v[o + 13], v[o + 14], v[o + 15], v[o + 16], v[o + 17], v[o + 18], v[o + 19],        \
+        v[o + 20], v[o + 21], v[o + 22], v[o + 23], v[o + 24], v[o + 25], v[o + 26], v[o + 27], v[o + 28],        \
+        v[o + 29], v[o + 30], v[o + 31]
+
+// 32 lanes x 32 consecutive columns of tensor memory, without the wait
+__device__ __forceinline__ void at_ld32(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void at_st32(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void at_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// bounded wait that gives up at once after another thread of the CTA did
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort_word)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    if (*abort_word)
+        return false;
+    if (mbar_wait(bar, parity, status))
+        return true;
+    *abort_word = 1;
+    return false;
+}
+
+// bounded wait until a stage has been armed for tile `n`
+__device__ __forceinline__ bool at_armed(volatile int *arm, int n, int32_t *status, volatile int *abort_word)
+{
+    if (*arm == n)
+        return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (*arm != n) {
+        __nanosleep(20);
+        if (*abort_word)
+            return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            flag_status(status, QMOE_DEV_TIMEOUT);
+            *abort_word = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// byte offset of 16-byte unit c of row r in an operand tile of `rows` rows
+__device__ __forceinline__ uint32_t at_sw(int rows, int r, int c)
+{
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// A unit that begins in a CTA and goes on in later ones, up to c1 (0: none).
+// The parts are 128 KB each and as many as the GPU has SMs, too much for one
+// CTA to add up (64 us for 9 parts when the last to arrive did it): a second
+// kernel joins them with the whole GPU, launched while this one runs.
+struct TcShared {
+    int c1, q0, row0, rows, h;
+};
+template <int M, int DP>
+__device__ __forceinline__ TcShared *tc_shared(const AttnArgs &a)
+{
+    return reinterpret_cast<TcShared *>(a.part + (size_t)kAttnMaxSms * 2 * M * (DP + 2));
+}
+
+// Keys that every row of a block sees: [lo_max, hi_min).
+__device__ __forceinline__ void at_limits(const AttnArgs &a, const AttnSeq &s, int row0, int rows, int &lo_max,
+                                          int &hi_min)
+{
+    int d;
+    attn_keys(a, s, row0 / a.group, d, hi_min);
+    attn_keys(a, s, (row0 + rows - 1) / a.group, lo_max, d);
+}
+
+template <class T, int DP, int NROW>
+__global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(const AttnArgs a, const __grid_constant__ AttnMaps maps)
+{
+    using C = TcCfg<DP, NROW>;
+    constexpr int KT = C::KT, M = C::M;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bar_off);
+    uint32_t *tmem_word = reinterpret_cast<uint32_t *>(smem + C::misc_off);
+    volatile int *abort_word = reinterpret_cast<volatile int *>(smem + C::misc_off + 4);
+    volatile int *poison = reinterpret_cast<volatile int *>(smem + C::misc_off + 16);   // [4], by unit
+    volatile int *armed_v = reinterpret_cast<volatile int *>(smem + C::misc_off + 32);  // [2], tile in the V stage
+    long long *scan = reinterpret_cast<long long *>(smem + C::misc_off + 64);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int W_MMA = C::SOFT / 32;
+
+    if (tid == 0) {
+        tc_shared<M, DP>(a)[blockIdx.x].c1 = 0;
+        const int full = a.tma ? 1 : C::LOAD;
+        mbar_init(&bar[TB_QF], a.tma ? C::FIX : C::LOAD);
+        mbar_init(&bar[TB_QE], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar[TB_KF + i], full);
+            mbar_init(&bar[TB_KE + i], 1);
+            mbar_init(&bar[TB_VF + i], full);
+            mbar_init(&bar[TB_VX + i], C::FIX);
+            mbar_init(&bar[TB_VE + i], 1);
+            mbar_init(&bar[TB_SF + i], 1);
+            mbar_init(&bar[TB_PF + i], 128);
+            mbar_init(&bar[TB_OF + i], 1);
+            mbar_init(&bar[TB_OE + i], 128);
+        }
+        mbar_init(&bar[TB_PV], 1);
+        mbar_init(&bar[TB_DRAIN], 1);
+        *abort_word = 0;
+        armed_v[0] = armed_v[1] = -1;
+        mbar_init_fence();
+    }
+    if (warp == W_MMA) {   // all of the SM's tensor memory (this warp frees it)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_word)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_trigger();   // the joining kernel may be launched; it waits for this one's end
+    const AttnSpan span = attn_span<M, KT, C::THREADS>(a, scan);
+    at_fence_before();
+    __syncthreads();
+    at_fence_after();
+    const uint32_t tmem = *tmem_word;
+    AttnWalk<M, KT> w;
+    w.start(a, span);
+
+    if (warp >= W_MMA) {
+        if (NROW == 2)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == W_MMA) {
+            // ================================================= MMA issuer
+            if (lane == 0) {
+                const uint32_t idesc_s = at_idesc<T>(KT, false);
+                const int n_o = (a.dim + 15) & ~15, ksteps = (a.dim + 15) / 16;
+                const uint32_t idesc_o = at_idesc<T>(n_o, true);
+                const uint32_t qb = smem_u32(smem + C::q_off), kb = smem_u32(smem + C::k_off),
+                               vb = smem_u32(smem + C::v_off);
+                uint32_t kc = 0, vc = 0, un = 0;          // tiles and units so far
+                uint32_t pc[2] = {0, 0}, oc[2] = {0, 0}, xc[2] = {0, 0};
+                bool ok = true, issued = false;
+                auto wait = [&](int b, uint32_t parity) {
+                    ok = ok && at_wait(&bar[b], parity & 1, a.status, abort_word);
+                    return ok;
+                };
+                auto scores = [&](int buf, int rt, uint32_t ks) {
+                    const uint32_t q = qb + rt * 128 * 128, k = kb + ks * C::tile;
+                    for (int i = 0; i < ksteps; ++i)
+                        at_mma_ss(tmem + C::s_col + buf * 128,
+                                  at_desc(q + (i >> 2) * M * 128 + (i & 3) * 32, 16),
+                                  at_desc(k + (i >> 2) * KT * 128 + (i & 3) * 32, 16), idesc_s, i > 0);
+                    at_commit(&bar[TB_SF + buf]);
+                    issued = true;
+                };
+                auto values = [&](int buf, int rt, uint32_t vs, bool acc) {
+                    const uint32_t v = vb + vs * C::tile;
+                    for (int i = 0; i < KT / 16; ++i)
+                        at_mma_ts(tmem + C::o_col + rt * DP, tmem + C::s_col + buf * 128 + i * 8,
+                                  at_desc(v + i * 2048, KT * 128), idesc_o, acc || i > 0);
+                };
+                for (; !w.done() && ok; w.next(a), ++un) {
+                    const int nt = w.tb() - w.ta();
+                    const int rows = min(M, w.s.n * a.group - w.rt * M);
+                    const int nr = NROW == 2 && rows > 128 ? 2 : 1;   // row tiles with rows
+                    int lo_max, hi_min;
+                    at_limits(a, w.s, w.rt * M, rows, lo_max, hi_min);
+                    if (!wait(TB_QF, un) || !wait(TB_KF + kc % 2, kc / 2))
+                        break;
+                    at_fence_after();
+                    for (int r = 0; r < nr; ++r)
+                        scores(NROW == 2 ? r : 0, r, kc % 2);
+                    at_commit(&bar[TB_KE + kc % 2]);
+                    ++kc;
+                    if (nt == 1)
+                        at_commit(&bar[TB_QE]);
+                    for (int j = 0; j < nt && ok; ++j, ++vc) {
+                        const bool more = j + 1 < nt;
+                        if (NROW == 1 && more) {
+                            if (!wait(TB_KF + kc % 2, kc / 2))
+                                break;
+                            at_fence_after();
+                            scores((j + 1) & 1, 0, kc % 2);
+                            at_commit(&bar[TB_KE + kc % 2]);
+                            ++kc;
+                            if (j + 2 == nt)
+                                at_commit(&bar[TB_QE]);
+                        }
+                        const int j0 = (w.t0 + w.ta() + j) * KT;
+                        if (a.tma && (j0 < lo_max || j0 + KT > hi_min)) {
+                            if (!wait(TB_VX + vc % 2, xc[vc % 2]))
+                                break;
+                            ++xc[vc % 2];
+                        } else if (!wait(TB_VF + vc % 2, vc / 2)) {
+                            break;
+                        }
+                        if (NROW == 2 && more && !wait(TB_KF + kc % 2, kc / 2))
+                            break;
+                        for (int r = 0; r < nr && ok; ++r) {
+                            const int buf = NROW == 2 ? r : j & 1;
+                            if (!wait(TB_PF + buf, pc[buf]))
+                                break;
+                            ++pc[buf];
+                            if (j == 0 && oc[r] > 0 && !wait(TB_OE + r, oc[r] - 1))
+                                break;   // the last unit's O has been read
+                            at_fence_after();
+                            values(buf, r, vc % 2, j > 0);
+                            if (NROW == 1)
+                                at_commit(&bar[TB_PV]);
+                            if (NROW == 2 && more)
+                                scores(buf, r, kc % 2);
+                            if (!more) {
+                                at_commit(&bar[TB_OF + r]);
+                                ++oc[r];
+                            }
+                        }
+                        at_commit(&bar[TB_VE + vc % 2]);
+                        if (NROW == 2 && more) {
+                            at_commit(&bar[TB_KE + kc % 2]);
+                            ++kc;
+                            if (j + 2 == nt)
+                                at_commit(&bar[TB_QE]);
+                        }
+                    }
+                }
+                if (issued) {   // nothing is in flight when the tensor memory is freed
+                    at_commit(&bar[TB_DRAIN]);
+                    mbar_wait(&bar[TB_DRAIN], 0, a.status);
+                }
+            }
+            __syncwarp();
+        } else {
+            // ==================================================== loaders
+            constexpr int CPR = DP / 8;
+            const int cpr = ((a.dim + 15) & ~15) / 8;   // 16-byte units that the products read
+            const uint32_t qs = smem_u32(smem + C::q_off);
+            bool dead = false;
+            // a block's query rows, by threads t of NT: each stays in its column
+            auto load_q = [&](int t, int nt, int row0, int rows) {
+                const int c = t % CPR;
+                const int tok0 = row0 / a.group, rem = row0 - tok0 * a.group;
+                const float inv = 1.f / a.group;
+                const bool in = c * 8 < a.dim;
+                if (c >= cpr)
+                    return;
+                const int rows_q = NROW == 2 && rows <= 128 ? 128 : M;
+#pragma unroll 4
+                for (int r = t / CPR; r < rows_q; r += nt / CPR) {
+                    // (rem + r) / group: exact, the quotient is half a step off a whole number
+                    const int dt = (int)((rem + r + 0.5f) * inv);
+                    const int hq = w.h * a.group + rem + r - dt * a.group;
+                    const bool live = in && r < rows;
+                    const long long e = (w.s.q0 + tok0 + dt) * a.q_token + hq * a.q_head + c * 8;
+                    cp_async16(qs + at_sw(M, r, c), a.q + (live ? e : 0), live);
+                }
+            };
+            // Keys that only some rows see, and keys outside the unit whose
+            // stale slots a TMA box brought along: a weight of zero times an
+            // infinite or NaN value would still reach the rows through the
+            // product.  Values outside the unit become zeros; infinite and NaN
+            // ones at the limits are taken out and added to the rows that see
+            // them at the end of the unit.
+            auto clean_v = [&](int stage, int j0, int lo_max, int hi_min, int u, int t, int nt) {
+                unsigned char *v = smem + C::v_off + stage * C::tile;
+                for (int e = t; e < KT * CPR; e += nt) {
+                    const int r = e / CPR, c = e % CPR, j = j0 + r;
+                    if (c >= cpr || (j >= lo_max && j < hi_min))
+                        continue;
+                    uint4 *q = reinterpret_cast<uint4 *>(v + at_sw(KT, r, c));
+                    if (j < w.lo || j >= w.hi) {
+                        *q = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 x = *q;
+                    uint32_t *p = reinterpret_cast<uint32_t *>(&x);
+                    bool bad = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (nonfinite2<T>(p[i])) {
+                            const float2 f = Num16<T>::up2(p[i]);
+                            p[i] = Num16<T>::down2(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
+                            bad = true;
+                        }
+                    if (bad) {
+                        *q = x;
+                        poison[u & 3] = 1;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            };
+            if (a.tma && warp == W_MMA + 1) {
+                // ---- TMA: each lane a box of the tile's keys
+                const int nbox = KT / a.tma, nblk = (a.dim + 63) / 64;
+                const uint32_t bytes = KT * 128 * nblk;
+                uint32_t n = 0, armed[2] = {0, 0};   // tiles so far, copies of K and V
+                if (lane == 0) {
+                    prefetch_tensormap(&maps.k);
+                    prefetch_tensormap(&maps.v);
+                }
+                for (; !w.done() && !dead; w.next(a)) {
+                    const int ta = w.ta(), tb = w.tb();
+                    long long box = lane < nbox ? attn_box(a, w.sp.b, (w.t0 + ta) * KT + lane * a.tma, w.lo, w.hi) : 0;
+                    for (int t = ta; t < tb && !dead; ++t, ++n) {
+                        const int page = (int)(box >> 32), slot = (int)(box & 0xFFFFFFFFll);
+                        if (t + 1 < tb && lane < nbox)   // on its way while this tile's copies go out
+                            box = attn_box(a, w.sp.b, (w.t0 + t + 1) * KT + lane * a.tma, w.lo, w.hi);
+                        for (int x = 0; x < 2 && !dead; ++x) {   // K, then V
+                            uint64_t *full = &bar[(x ? TB_VF : TB_KF) + n % 2];
+                            if (n >= 2 && !__all_sync(0xffffffffu, at_wait(&bar[(x ? TB_VE : TB_KE) + n % 2],
+                                                                           (n / 2 - 1) & 1, a.status, abort_word))) {
+                                dead = true;
+                                break;
+                            }
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(full, bytes);
+                                if (x == 1)
+                                    armed_v[n % 2] = (int)n;
+                            }
+                            ++armed[x];
+                            __syncwarp();
+                            const uint32_t dst = smem_u32(smem + (x ? C::v_off : C::k_off) + (n % 2) * C::tile) +
+                                                 lane * a.tma * 128;
+                            if (lane < nbox)
+                                for (int k = 0; k < nblk; ++k)
+                                    tma_load_4d(dst + k * KT * 128, x ? &maps.v : &maps.k, k * 64,
+                                                a.heads_inner ? w.h : slot, a.heads_inner ? slot : w.h, page, full);
+                            __syncwarp();
+                        }
+                    }
+                }
+                // no copy may still be landing when the CTA exits
+                if (lane == 0)
+                    for (int x = 0; x < 2; ++x)
+                        for (uint32_t i = armed[x] > 2 ? armed[x] - 2 : 0; i < armed[x]; ++i)
+                            mbar_wait(&bar[(x ? TB_VF : TB_KF) + i % 2], (i / 2) & 1, a.status);
+                __syncwarp();
+            } else if (a.tma) {
+                // ---- beside it: the query rows, and V at the limits
+                const int t = tid - C::SOFT - 64;
+                uint32_t un = 0, n = 0;
+                for (; !w.done(); w.next(a), ++un) {
+                    const int ta = w.ta(), tb = w.tb();
+                    const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
+                    if (un > 0 && !at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))
+                        dead = true;
+                    if (bar_any(TC_BAR_LOAD, C::FIX, dead))
+                        break;
+                    if (t == 0)
+                        poison[un & 3] = 0;
+                    load_q(t, C::FIX, row0, rows);
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&bar[TB_QF]);
+                    named_bar_sync(TC_BAR_LOAD, C::FIX);   // the cleared poison flag is seen
+                    int lo_max, hi_min;
+                    at_limits(a, w.s, row0, rows, lo_max, hi_min);
+                    for (int i = ta; i < tb && !dead; ++i) {
+                        const int j0 = (w.t0 + i) * KT;
+                        if (j0 >= lo_max && j0 + KT <= hi_min)
+                            continue;
+                        const uint32_t s = n + (i - ta);
+                        // armed first: a parity tells two uses of a stage apart only
+                        // once the earlier one is over
+                        if (!at_armed(&armed_v[s % 2], (int)s, a.status, abort_word) ||
+                            !at_wait(&bar[TB_VF + s % 2], (s / 2) & 1, a.status, abort_word)) {
+                            dead = true;
+                            break;
+                        }
+                        clean_v(s % 2, j0, lo_max, hi_min, un, t, C::FIX);
+                        mbar_arrive(&bar[TB_VX + s % 2]);
+                    }
+                    n += tb - ta;
+                }
+            } else {
+                // ---- cp.async
+                const int lt = tid - C::SOFT - 32;
+                long long *off = reinterpret_cast<long long *>(smem + C::off_off);
+                uint32_t kc = 0, un = 0;
+                // copies in flight, oldest first: the barrier to arrive at and, for
+                // a V tile with keys that only some rows see, where it lies
+                int pend_bar[3] = {0, 0, 0}, pend_j0[3] = {-1, -1, -1}, np = 0;
+                int lo_max = 0, hi_min = 0;
+                auto finish = [&](int i) {
+                    if (pend_j0[i] >= 0)
+                        clean_v(pend_bar[i] - TB_VF, pend_j0[i], lo_max, hi_min, un, lt, C::LOAD);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(&bar[pend_bar[i]]);
+                };
+                auto flush = [&]() {
+                    cp_async_wait<0>();
+                    for (int i = 0; i < np; ++i)
+                        finish(i);
+                    np = 0;
+                };
+                auto push = [&](int b, int j0) {
+                    cp_async_commit();
+                    pend_bar[np] = b;
+                    pend_j0[np] = j0;
+                    if (++np == 3) {
+                        cp_async_wait<2>();
+                        finish(0);
+                        pend_bar[0] = pend_bar[1];
+                        pend_bar[1] = pend_bar[2];
+                        pend_j0[0] = pend_j0[1];
+                        pend_j0[1] = pend_j0[2];
+                        np = 2;
+                    }
+                };
+                // the slot of the n-th use of a barrier pair is free again; what is
+                // in flight is handed over before blocking
+                auto acquire = [&](int b, uint32_t n, uint32_t stages) {
+                    if (n < stages || dead)
+                        return;
+                    const uint32_t parity = (n / stages - 1) & 1;
+                    if (mbar_try_wait_now(&bar[b], parity))
+                        return;
+                    flush();
+                    if (!at_wait(&bar[b], parity, a.status, abort_word))
+                        dead = true;
+                };
+                auto slot = [&](int t, int tb, int r) {
+                    const int j = (w.t0 + t) * KT + r;
+                    long long o = -1;
+                    if (r < KT && t < tb && j >= w.lo && j < w.hi) {
+                        o = attn_slot(a, w.sp.b, w.h, j);
+                        if (o < 0)
+                            flag_status(a.status, QMOE_DEV_BAD_PAGE);
+                    }
+                    return o;
+                };
+                for (; !w.done(); w.next(a), ++un) {
+                    const int ta = w.ta(), tb = w.tb();
+                    const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
+                    long long o0 = slot(ta, tb, lt), o1 = slot(ta, tb, lt + C::LOAD);
+                    acquire(TB_QE, un, 1);
+                    at_limits(a, w.s, row0, rows, lo_max, hi_min);
+                    if (bar_any(TC_BAR_LOAD, C::LOAD, dead || *abort_word != 0))
+                        break;
+                    if (lt == 0)
+                        poison[un & 3] = 0;
+                    load_q(lt, C::LOAD, row0, rows);
+                    push(TB_QF, -1);
+                    for (int t = ta; t < tb; ++t, ++kc) {
+                        long long *o = off + (t & 1) * KT;
+                        if (lt < KT)
+                            o[lt] = o0;
+                        if (lt + C::LOAD < KT)
+                            o[lt + C::LOAD] = o1;
+                        // (the barrier also keeps the loaders together after a timeout)
+                        if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
+                            break;
+                        o0 = slot(t + 1, tb, lt);
+                        o1 = slot(t + 1, tb, lt + C::LOAD);
+                        for (int x = 0; x < 2; ++x) {   // K, then V
+                            const int fb = (x ? TB_VF : TB_KF) + (int)(kc % 2);
+                            acquire((x ? TB_VE : TB_KE) + (int)(kc % 2), kc, 2);
+                            if (dead)
+                                break;
+                            const uint32_t dst = smem_u32(smem + (x ? C::v_off : C::k_off) + (kc % 2) * C::tile);
+                            const uint16_t *base = x ? a.v : a.k;
+                            // a thread stays in its column; 8 rows' offsets are read
+                            // before their copies go out, so that no copy waits for
+                            // shared memory
+                            constexpr int RP = C::LOAD / CPR;   // rows per pass
+                            const int c = lt % CPR;
+                            if (c < cpr) {
+                                const bool in = c * 8 < a.dim;
+                                for (int r0 = lt / CPR; r0 < KT; r0 += 8 * RP) {
+                                    long long s[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        s[i] = r0 + i * RP < KT ? o[r0 + i * RP] : 0;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        if (r0 + i * RP < KT) {
+                                            const bool live = in && s[i] >= 0;
+                                            cp_async16(dst + at_sw(KT, r0 + i * RP, c),
+                                                       base + (live ? s[i] + c * 8 : 0), live);
+                                        }
+                                }
+                            }
+                            const int j0 = (w.t0 + t) * KT;
+                            const bool some = (j0 < lo_max && j0 + KT > w.lo) || (j0 + KT > hi_min && j0 < w.hi);
+                            push(fb, x && some ? j0 : -1);
+                        }
+                    }
+                    flush();   // this unit's V is looked over with its own rows' limits
+                    if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
+                        break;
+                }
+            }
+        }
+    } else {
+        // ====================================================== softmax
+        if (NROW == 2)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int rt = warp >> 2, quad = warp & 3;
+        const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
+        const int rr = rt * 128 + quad * 32 + lane;   // row of the unit
+        uint32_t sc[2] = {0, 0}, oc = 0, pv = 0, un = 0;
+        bool dead = false;
+        const float sc2 = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
+        const float capc = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : 0.f, cap = a.softcap * kLog2e;
+        for (; !w.done(); w.next(a), ++un) {
+            const int ta = w.ta(), tb = w.tb();
+            const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
+            const bool active = rt * 128 < rows;
+            const bool whole = ta == 0 && tb == w.nt;
+            int lo = 0, hi = 0;
+            const int tok = (row0 + rr) / a.group, hq = w.h * a.group + (row0 + rr) - tok * a.group;
+            if (rr < rows)
+                attn_keys(a, w.s, tok, lo, hi);
+            float m = -INFINITY, l = 0.f;
+            if (active) {
+                for (int t = ta; t < tb && !dead; ++t) {
+                    const int buf = NROW == 2 ? rt : (t - ta) & 1;
+                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_SF + buf], sc[buf] & 1, a.status, abort_word))) {
+                        dead = true;
+                        break;
+                    }
+                    ++sc[buf];
+                    at_fence_after();
+                    const uint32_t ts = tq + C::s_col + buf * 128;
+                    uint32_t s[KT];
+#pragma unroll
+                    for (int c = 0; c < KT; c += 32)
+                        at_ld32(ts + c, s + c);
+                    at_wait_ld();
+                    const int j0 = (w.t0 + t) * KT;
+                    if (a.softcap > 0.f) {
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            s[c] = __float_as_uint(capped(__uint_as_float(s[c]), capc, cap));
+                    }
+                    const int l0 = lo - j0, h0 = hi - j0;
+                    if (__any_sync(0xffffffffu, l0 > 0 || h0 < KT)) {
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            if (c < l0 || c >= h0)
+                                s[c] = 0xFF800000u;   // -inf
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; ++c)
+                        mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc2;
+                    const bool grow = top > m + TC_LAZY || (m == -INFINITY && top > m);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float mn = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (t > ta) {
+                            // O holds the products up to the last tile's
+                            if (NROW == 1 &&
+                                !__all_sync(0xffffffffu, at_wait(&bar[TB_PV], (pv - 1) & 1, a.status, abort_word))) {
+                                dead = true;
+                                break;
+                            }
+                            at_fence_after();
+                            const uint32_t to = tq + C::o_col + rt * DP;
+                            for (int c = 0; c < a.dim; c += 32) {
+                                uint32_t v[32];
+                                at_ld32(to + c, v);
+                                at_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                                at_st32(to + c, v);
+                            }
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < KT; c += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x = exp2_approx(fmaf(__uint_as_float(s[c + 2 * i]), sc2, -base));
+                            const float y = exp2_approx(fmaf(__uint_as_float(s[c + 2 * i + 1]), sc2, -base));
+                            sum[(2 * i) & 3] += x;
+                            sum[(2 * i + 1) & 3] += y;
+                            // the weights enter the product in the cache's type (at
+                            // most half a step each); their sum stays unrounded
+                            p[i] = Num16<T>::down2(x, y);
+                        }
+                        at_st32(ts + c / 2, p);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    at_wait_st();
+                    at_fence_before();
+                    mbar_arrive(&bar[TB_PF + buf]);
+                    ++pv;
+                }
+                // ---- the row's output
+                if (!dead && !__all_sync(0xffffffffu, at_wait(&bar[TB_OF + rt], oc & 1, a.status, abort_word)))
+                    dead = true;
+                if (!dead) {
+                    ++oc;
+                    at_fence_after();
+                    const uint32_t to = tq + C::o_col + rt * DP;
+                    float *part = attn_part<M, DP>(a, blockIdx.x, ta == 0);
+                    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                    const bool bad = poison[un & 3] != 0;
+                    int lo_max = 0, hi_min = 0;
+                    if (bad)
+                        at_limits(a, w.s, row0, rows, lo_max, hi_min);
+                    for (int c = 0; c < a.dim; c += 32) {
+                        uint32_t v[32];
+                        at_ld32(to + c, v);
+                        at_wait_ld();
+                        if (rr >= rows)
+                            continue;
+                        if (bad) {   // the values taken out by the loaders, for the rows that see them
+                            const int j1 = min(hi, (w.t0 + tb) * KT);
+                            for (int j = max(lo, (w.t0 + ta) * KT); j < j1; ++j) {
+                                if (j >= lo_max && j < hi_min) {
+                                    j = hi_min - 1;
+                                    continue;
+                                }
+                                const long long e = attn_slot(a, w.sp.b, w.h, j);
+                                if (e < 0)
+                                    continue;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (c + i < a.dim) {
+                                        const float x = Num16<T>::up(a.v[e + c + i]);
+                                        if (!isfinite(x))
+                                            v[i] = __float_as_uint(__uint_as_float(v[i]) + x);
+                                    }
+                            }
+                        }
+                        if (whole) {
+                            uint16_t *dst = a.out + (w.s.q0 + tok) * a.o_token + hq * a.o_head + c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 8)
+                                if (c + i < a.dim) {
+                                    uint4 u;
+                                    u.x = Num16<T>::down2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+                                    u.y = Num16<T>::down2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
+                                    u.z = Num16<T>::down2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
+                                    u.w = Num16<T>::down2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
+                                    *reinterpret_cast<uint4 *>(dst + i) = u;
+                                }
+                        } else {
+                            float *dst = part + (size_t)rr * DP + c;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4)
+                                if (c + i < a.dim)
+                                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        }
+                    }
+                    at_fence_before();
+                    mbar_arrive(&bar[TB_OE + rt]);
+                    if (rr < rows) {
+                        if (whole) {
+                            if (a.lse)
+                                a.lse[(size_t)(w.s.q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                        } else {
+                            part[M * DP + rr] = m;
+                            part[M * DP + M + rr] = l;
+                        }
+                    }
+                }
+            }
+            // the softmax warpgroups leave together
+            if (bar_any(TC_BAR_SOFT, C::SOFT, dead))
+                break;
+            if (tid == 0 && ta == 0 && tb < w.nt) {   // begins here, goes on in later CTAs
+                TcShared *d = tc_shared<M, DP>(a) + blockIdx.x;
+                d->q0 = w.s.q0;
+                d->row0 = row0;
+                d->rows = rows;
+                d->h = w.h;
+                d->c1 = attn_cta(w.sp, w.u0 + w.nt - 1);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == W_MMA) {
+        at_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    }
+}
+
+// Joins the parts of the units that several CTAs shared: CTA (x, y) takes 32
+// rows of the unit that begins in CTA x, a warp a row at a time.
+constexpr int TJ_ROWS = 32, TJ_THREADS = 256;
+
+template <class T, int DP, int M>
+__global__ void __launch_bounds__(TJ_THREADS) attn_join_kernel(const AttnArgs a)
+{
+    pdl_wait();
+    const TcShared d = tc_shared<M, DP>(a)[blockIdx.x];
+    if (d.c1 == 0)
+        return;
+    const int r1 = min((int)blockIdx.y * TJ_ROWS + TJ_ROWS, d.rows);
+    for (int r = blockIdx.y * TJ_ROWS + (threadIdx.x >> 5); r < r1; r += TJ_THREADS / 32)
+        attn_join_row<T, M, DP>(a, blockIdx.x, d.c1, r, d.q0, d.row0 + r, d.h);
+}
+
+template <class T, int DP, int NROW>
+cudaError_t launch_tc(const AttnArgs &args, const LaunchCfg &c)
+{
+    using C = TcCfg<DP, NROW>;
+    AttnArgs a = args;
+    AttnMaps maps = {};
+    if (!attn_maps(a, Num16<T>::kExp == 0x7F807F80u, C::KT, &maps, &a.tma, &a.heads_inner))
+        a.tma = 0;
+    auto kern = attn_tc_kernel<T, DP, NROW>;
+    cudaError_t e = set_smem(kern, C::total);
+    if (e != cudaSuccess)
+        return e;
+    LaunchCfg c2 = c;
+    c2.pdl = false;
+    e = launch_ex(kern, dim3(c.num_sms), dim3(C::THREADS), C::total, c2, 1, a, maps);
+    if (e != cudaSuccess)
+        return e;
+    // always as a dependent: it waits for the parts itself
+    c2.pdl = true;
+    return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / TJ_ROWS), dim3(TJ_THREADS), 0, c2, 1, a);
+}
+
+template <class T>
+cudaError_t launch_t(const AttnArgs &a, int row_tiles, const LaunchCfg &c)
+{
+    if (a.dim <= 64)
+        return row_tiles == 2 ? launch_tc<T, 64, 2>(a, c) : launch_tc<T, 64, 1>(a, c);
+    if (a.dim <= 128)
+        return row_tiles == 2 ? launch_tc<T, 128, 2>(a, c) : launch_tc<T, 128, 1>(a, c);
+    return launch_tc<T, 256, 1>(a, c);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, int row_tiles, const LaunchCfg &c)
+{
+    return bf16 ? launch_t<__nv_bfloat16>(a, row_tiles, c) : launch_t<__half>(a, row_tiles, c);
+}
+
+}  // namespace qmoe

@@ -292,6 +292,20 @@ __device__ __forceinline__ long long attn_slot(const AttnArgs &a, int b, int h, 
     return id * a.page_stride + (long long)(j - pg * a.page_size) * a.token_stride + h * a.head_stride;
 }
 
+// one look at a barrier, without being parked
+__device__ __forceinline__ bool mbar_try_wait_now(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0)
@@ -302,6 +316,45 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ----------------------------------------------------------------- TMA --
+// Tensor maps of the cache: boxes of 64 columns x a.tma slots of one page and
+// head, 128-byte swizzled.
+struct AttnMaps {
+    CUtensorMap k, v;
+};
+
+// False where the cache's shape has no such map: pages must divide into
+// boxes of a multiple of 8 slots (the swizzle's period) that divide a tile of
+// kt keys, and the strides must nest.
+bool attn_maps(const AttnArgs &a, bool bf16, int kt, AttnMaps *m, int *rows, int *heads_inner);
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c0, int c1, int c2, int c3,
+                                            uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// keys [j, j + a.tma) of sequence b: where they lie, packed as page << 32 |
+// slot; page a.num_pages (beyond the cache: the copy writes zeros) where the
+// unit reads none of them or the page id is bad
+__device__ __forceinline__ long long attn_box(const AttnArgs &a, int b, int j, int lo, int hi)
+{
+    const int pg = (int)((unsigned)j / (unsigned)a.page_size);
+    int id = a.num_pages;
+    if (j < hi && j + a.tma > lo) {
+        id = __ldg(a.table + (size_t)b * a.max_pages + pg);
+        if ((unsigned)id >= (unsigned)a.num_pages) {
+            flag_status(a.status, QMOE_DEV_BAD_PAGE);
+            id = a.num_pages;
+        }
+    }
+    return ((long long)id << 32) | (uint32_t)(j - pg * a.page_size);
 }
 
 // ----------------------------------------------------------------- joining --
@@ -315,12 +368,13 @@ __device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, int slot
 }
 
 // Announces this CTA's part of a unit that CTAs c0..c1 share; true for the
-// last one, which then reads all parts.  All NT threads of the CTA.
+// last one, which then reads all parts.  The first NT threads of the CTA, on
+// named barrier 1.
 template <int NT>
 __device__ __forceinline__ bool attn_arrive(const AttnArgs &a, int c0, int c1, int *sm)
 {
     __threadfence();
-    __syncthreads();
+    named_bar_sync(1, NT);
     if (threadIdx.x == 0) {
         const int got = atomicAdd(a.ctr + c0, 1);
         *sm = got == c1 - c0;
@@ -328,46 +382,85 @@ __device__ __forceinline__ bool attn_arrive(const AttnArgs &a, int c0, int c1, i
             a.ctr[c0] = 0;
         __threadfence();
     }
-    __syncthreads();
+    named_bar_sync(1, NT);
     return *sm != 0;
 }
 
-// out / lse of one unit row from its parts c0..c1, 4 columns a thread
-template <class T, int M, int DP, int NT>
-__device__ __forceinline__ void attn_join(const AttnArgs &a, const AttnSeq &s, int rt, int h, int c0, int c1)
+// One row's output from the parts c0..c1 of its unit, by one warp: a lane
+// reads the maximum and sum of one part each, the parts' weights go round by
+// shuffles, and DP / 32 columns a lane are added in the parts' order.  r: row
+// of the unit; row: of the sequence, whose first token is row q0.
+template <class T, int M, int DP>
+__device__ __forceinline__ void attn_join_row(const AttnArgs &a, int c0, int c1, int r, int q0, int row, int h)
 {
-    const int rows = min(M, s.n * a.group - rt * M);
-    const int d4 = a.dim / 4;
-    const int nseg = c1 - c0 + 1;
-    for (int i = threadIdx.x; i < rows * d4; i += NT) {
-        const int r = i / d4, d = (i - r * d4) * 4;
-        float m = -INFINITY;
-        for (int k = 0; k < nseg; ++k)
-            m = fmaxf(m, __ldcg(attn_part<M, DP>(a, c0 + k, k == 0) + M * DP + r));
-        const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < nseg; ++k) {
-            const float *p = attn_part<M, DP>(a, c0 + k, k == 0);
-            const float w = exp2_approx(__ldcg(p + M * DP + r) - base);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + (size_t)r * DP + d));
-            l = fmaf(w, __ldcg(p + M * DP + M + r), l);
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
+    const int lane = threadIdx.x & 31, np = c1 - c0 + 1;
+    constexpr int V = DP / 32;
+    float m = -INFINITY, l = 0.f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        o[i] = 0.f;
+    for (int k0 = 0; k0 < np; k0 += 32) {
+        const int k = k0 + lane;
+        const float *p = attn_part<M, DP>(a, c0 + (k < np ? k : 0), k == 0 || k >= np);
+        const float mk = k < np ? __ldcg(p + M * DP + r) : -INFINITY;
+        const float lk = k < np ? __ldcg(p + M * DP + M + r) : 0.f;
+        const int n = min(32, np - k0);
+        float w = 0.f;
+        // 8 parts' columns are on their way at once, the first 8 beside the maxima
+        for (int x0 = 0; x0 < n; x0 += 8) {
+            float v[8][V];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int kk = k0 + x0 + x;
+                const float *q = attn_part<M, DP>(a, c0 + kk, kk == 0) + (size_t)r * DP + lane * V;
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    float2 u = make_float2(0.f, 0.f);
+                    if (x0 + x < n)
+                        u = __ldcg(reinterpret_cast<const float2 *>(q + i));
+                    v[x][i] = u.x;
+                    v[x][i + 1] = u.y;
+                }
+            }
+            if (x0 == 0) {
+                float top = mk;
+#pragma unroll
+                for (int s = 16; s; s >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+                top = fmaxf(top, m);
+                const float base = top == -INFINITY ? 0.f : top;
+                const float f = exp2_approx(m - base);
+                w = exp2_approx(mk - base);
+                float sum = w * lk;
+#pragma unroll
+                for (int s = 16; s; s >>= 1)
+                    sum += __shfl_xor_sync(0xffffffffu, sum, s);
+                l = l * f + sum;
+                m = top;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    o[i] *= f;
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float wx = __shfl_sync(0xffffffffu, w, x0 + x);
+                if (x0 + x < n) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        o[i] = fmaf(wx, v[x][i], o[i]);
+                }
+            }
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = rt * M + r;
-        const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
-        uint2 w2;
-        w2.x = Num16<T>::down2(o.x * inv, o.y * inv);
-        w2.y = Num16<T>::down2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2 *>(a.out + (size_t)(s.q0 + tok) * a.o_token + (size_t)hq * a.o_head + d) = w2;
-        if (a.lse && d == 0)
-            a.lse[(size_t)(s.q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+    uint16_t *dst = a.out + (q0 + tok) * a.o_token + hq * a.o_head + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        if (lane * V + i < a.dim)
+            *reinterpret_cast<uint32_t *>(dst + i) = Num16<T>::down2(o[i] * inv, o[i + 1] * inv);
+    if (a.lse && lane == 0)
+        a.lse[(size_t)(q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace qmoe

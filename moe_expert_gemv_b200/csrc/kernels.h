@@ -243,6 +243,8 @@ struct AttnArgs {
     int page_size, num_pages, max_pages;
     float scale, softcap;
     int window, causal;
+    int tma;                         // rows of a TMA box of the cache, 0: none can be used
+    int heads_inner;                 // order of the map's middle dimensions: heads, then slots
     float *part;                     // partial results of units that several CTAs share
     int *ctr;                        // their arrival counters, zero between calls
     int32_t *status;
@@ -250,8 +252,10 @@ struct AttnArgs {
 // rows (tokens x query heads of one K/V head) of the longest sequence decide
 // the row block; `bf16` the type
 cudaError_t launch_attn(const AttnArgs &a, bool bf16, long long max_rows, const LaunchCfg &c);
+// attention_tc.cu: row_tiles 1 or 2 tiles of 128 rows per unit
+cudaError_t launch_attn_tc(const AttnArgs &a, bool bf16, int row_tiles, const LaunchCfg &c);
 size_t attn_workspace_bytes(int dim, long long max_rows);
-constexpr int kAttnMaxCtas = 480;            // at most 3 CTAs on each of 160 SMs
+constexpr int kAttnMaxSms = 160;             // at most 3 CTAs on each
 constexpr size_t kAttnCounterBytes = 4096;   // one int32 arrival counter per CTA
 
 // ----------------------------------------------- rotary positions, append --

@@ -9,6 +9,7 @@ is missing or the device is not an sm_100 GPU the calls fail loudly.
 """
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -695,18 +696,32 @@ class CLogitRules(ctypes.Structure):
                 ("max_bias", ctypes.c_int32)]
 
 
+def _packer(cls):
+    """pack(*values) -> bytes laid out as the structure (nested ones flat):
+    built several times as fast as a ctypes structure, which shows in a decode
+    step's calls."""
+    code = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    flat = lambda c: "".join(code[t] if t in code else flat(t) for _, t in c._fields_)  # noqa: E731
+    return struct.Struct("@" + flat(cls)).pack
+
+
+_pack_rows, _pack_attn, _pack_rules = _packer(CRows), _packer(CAttn), _packer(CLogitRules)
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _device_call(fn, what, device, *args):
     """fn(*args, current stream of `device`) with `device` current."""
-    if device.index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch._C._cuda_getDevice():
+        code = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            code = fn(*args, _raw_stream(device))
     if code != OK:
         raise QmoeError(code, what)
 
@@ -720,21 +735,31 @@ def _on(device, t, what):
 def _opt(t, dtype, what, shape, device):
     """Address of an optional contiguous tensor (None: 0)."""
     if t is None:
-        return None
-    return _on(device, _need(t, dtype, what, shape), what).data_ptr()
+        return 0
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError("%s must be a %s tensor" % (what, dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous and have shape %s" % (what, tuple(shape)))
+    return _on(device, t, what).data_ptr()
+
+
+def _status(t, device):
+    """Address of an optional status word."""
+    return None if t is None else _opt(t, torch.int32, "status", t.shape, device)
 
 
 def _rows(t, what, dtype, device, shape):
-    """A [tokens][heads][dim] tensor of any token and head strides."""
+    """Address, token and head stride of a [tokens][heads][dim] tensor of any
+    token and head strides."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
         raise TypeError("%s must be a %s tensor on %s" % (what, dtype, device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    st = t.stride()
-    if st[2] != 1 and shape[2] > 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] > 1:
         raise ValueError("%s: the elements of a head must follow each other" % what)
     # the stride of a dimension of one element says nothing
-    return CRows(t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0)
+    return t.data_ptr(), s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0
 
 
 class KVCache:
@@ -828,13 +853,14 @@ def rope_rotate(rope, x, positions, out=None, status=None):
     dev = _on(rope.device, x, "x").device
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    cx, co = _rows(x, "x", x.dtype, dev, x.shape), _rows(out, "out", x.dtype, dev, x.shape)
+    x_ptr, x_token, x_head = _rows(x, "x", x.dtype, dev, x.shape)
+    o_ptr, o_token, o_head = _rows(out, "out", x.dtype, dev, x.shape)
     T, H, D = x.shape
     if x.numel() == 0:   # empty tensors have no address
         return out
-    _device_call(lib().rope_rotate, "rope_rotate", dev, rope._ref, cx.data, cx.token_stride, cx.head_stride,
-                 _DTYPES[x.dtype], T, H, D, _opt(positions, torch.int32, "positions", (T,), dev), co.data,
-                 co.token_stride, co.head_stride, _ptr(status))
+    _device_call(lib().rope_rotate, "rope_rotate", dev, rope._ref, x_ptr, x_token, x_head, _DTYPES[x.dtype],
+                 T, H, D, _opt(positions, torch.int32, "positions", (T,), dev), o_ptr, o_token, o_head,
+                 _status(status, dev))
     return out
 
 
@@ -848,23 +874,22 @@ def kv_append(cache, batch, k, v, q=None, rope=None, positions=None, q_out=None,
         raise ValueError("cache, batch and rope must be on one device")
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    ck, cv = _rows(k, "k", dt, dev, shape), _rows(v, "v", dt, dev, shape)
+    ck, cv = _pack_rows(*_rows(k, "k", dt, dev, shape)), _pack_rows(*_rows(v, "v", dt, dev, shape))
     cq = co = None
     heads = 0
     if q is not None:
         if rope is None:
             raise ValueError("q needs rope")
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
         heads = q.shape[1]
         shape = (T, heads, cache.head_dim)
-        cq = ctypes.byref(_rows(q, "q", dt, dev, shape))
-        co = ctypes.byref(_rows(q_out, "q_out", dt, dev, shape))
+        cq = _pack_rows(*_rows(q, "q", dt, dev, shape))
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dt, device=dev)
+        co = _pack_rows(*_rows(q_out, "q_out", dt, dev, shape))
     if T == 0:   # empty tensors have no address
         return q_out
     _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T), rope._ref if rope else None,
-                 _opt(positions, torch.int32, "positions", (T,), dev), cq, co, heads, ctypes.byref(ck),
-                 ctypes.byref(cv), _ptr(status))
+                 _opt(positions, torch.int32, "positions", (T,), dev), cq, co, heads, ck, cv, _status(status, dev))
     return q_out
 
 
@@ -883,15 +908,21 @@ def attn_workspace(head_dim, max_rows, device="cuda"):
     return ws
 
 
-def _attn_workspace(head_dim, max_rows, device, stream):
+_attn_need = {}
+
+
+def _attn_workspace(head_dim, max_rows, device):
     """One workspace for each stream; in a capture one of the graph's own (its
     zeros are set by the graph)."""
     if torch.cuda.is_current_stream_capturing():
         return attn_workspace(head_dim, max_rows, device)
-    need = lib().attn_paged_workspace_bytes(head_dim, max_rows)
-    ws = _attn_ws.get((device.index, stream))
+    need = _attn_need.get((head_dim, max_rows))
+    if need is None:
+        need = _attn_need[head_dim, max_rows] = lib().attn_paged_workspace_bytes(head_dim, max_rows)
+    key = (device.index, _raw_stream(device))
+    ws = _attn_ws.get(key)
     if ws is None or ws.numel() < need:
-        ws = _attn_ws[(device.index, stream)] = attn_workspace(head_dim, max_rows, device)
+        ws = _attn_ws[key] = attn_workspace(head_dim, max_rows, device)
     return ws
 
 
@@ -909,25 +940,24 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
         raise TypeError("q must be a tensor [tokens][heads][dim]")
     T, H, D = q.shape
     shape = (T, H, cache.head_dim)
-    cq = _rows(q, "q", cache.dtype, dev, shape)
+    q_ptr, q_token, q_head = _rows(q, "q", cache.dtype, dev, shape)
     if out is None:
         out = torch.empty(shape, dtype=cache.dtype, device=dev)
-        co = CRows(out.data_ptr(), H * D, D)
+        o_ptr, o_token, o_head = out.data_ptr(), H * D, D
     else:
-        co = _rows(out, "out", cache.dtype, dev, shape)
+        o_ptr, o_token, o_head = _rows(out, "out", cache.dtype, dev, shape)
     if lse is None and want_lse:
         lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-    rows = max((batch.max_new or T) * (H // cache.kv_heads), 1)
-    if workspace is None:
-        workspace = _attn_workspace(D, rows, dev, torch.cuda.current_stream(dev).cuda_stream)
-    else:
-        _on(dev, workspace, "workspace")
-    c = CAttn(cq, co, _opt(lse, torch.float32, "lse", (T, H), dev), H, window, 1 if causal else 0,
-              D ** -0.5 if scale is None else scale, softcap)
     if T == 0:   # empty tensors have no address
         return out if lse is None else (out, lse)
-    _device_call(lib().attn_paged, "attn_paged", dev, ctypes.addressof(c), cache._ref, batch._c(T),
-                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status))
+    if workspace is None:
+        workspace = _attn_workspace(D, max((batch.max_new or T) * (H // cache.kv_heads), 1), dev)
+    else:
+        _on(dev, workspace, "workspace")
+    c = _pack_attn(q_ptr, q_token, q_head, o_ptr, o_token, o_head, _opt(lse, torch.float32, "lse", (T, H), dev), H,
+                   window, 1 if causal else 0, D ** -0.5 if scale is None else scale, softcap)
+    _device_call(lib().attn_paged, "attn_paged", dev, c, cache._ref, batch._c(T), workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), _status(status, dev))
     return out if lse is None else (out, lse)
 
 
@@ -951,37 +981,40 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
     _on(dev, out, "out")
     if V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
         raise ValueError("a row's logits must follow each other")
-    c = CLogitRules()
+    hist = hist_stride = max_hist = mask_ptr = mask_stride = max_bias = 0
     if history is not None:
         if history.dim() != 2 or history.shape[0] != R or history.dtype != torch.int32 or \
                 (history.shape[1] > 1 and history.stride(1) != 1):
             raise ValueError("history must be int32 [rows][tokens], the tokens of a row one after the other")
-        c.history, c.history_stride, c.max_history = _on(dev, history, "history").data_ptr(), history.stride(0), history.shape[1]
         if history_len is None:
             raise ValueError("history needs history_len")
-        c.history_len = _opt(history_len, torch.int32, "history_len", (R,), dev)
-        c.prompt_len = _opt(prompt_len, torch.int32, "prompt_len", (R,), dev)
+        max_hist = history.shape[1]
+        hist, hist_stride = _on(dev, history, "history").data_ptr(), history.stride(0) if R > 1 else max_hist
     elif any(t is not None for t in (history_len, prompt_len, repetition, presence, frequency)):
         raise ValueError("penalties need history")
-    c.repetition = _opt(repetition, torch.float32, "repetition", (R,), dev)
-    c.presence = _opt(presence, torch.float32, "presence", (R,), dev)
-    c.frequency = _opt(frequency, torch.float32, "frequency", (R,), dev)
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias and bias_ids go together")
     if bias is not None:
-        c.max_bias = bias.shape[-1]
-        c.bias_ids = _opt(bias_ids, torch.int32, "bias_ids", (R, c.max_bias), dev)
-        c.bias = _opt(bias, torch.float32, "bias", (R, c.max_bias), dev)
+        max_bias = bias.shape[-1]
     if mask is not None:
         _need(mask, torch.int32, "mask")
         words = (V + 31) // 32
         if mask.dim() != 2 or mask.shape[0] not in (1, R) or mask.shape[1] < words:
             raise ValueError("mask must be int32 [rows] or [1] x at least %d words" % words)
-        c.mask, c.mask_stride = _on(dev, mask, "mask").data_ptr(), mask.shape[1] if mask.shape[0] == R else 0
+        mask_ptr = _on(dev, mask, "mask").data_ptr()
+        mask_stride = mask.shape[1] if mask.shape[0] == R else 0
+    rows = (R,)
+    c = _pack_rules(hist, _opt(history_len, torch.int32, "history_len", rows, dev),
+                    _opt(prompt_len, torch.int32, "prompt_len", rows, dev), hist_stride,
+                    _opt(repetition, torch.float32, "repetition", rows, dev),
+                    _opt(presence, torch.float32, "presence", rows, dev),
+                    _opt(frequency, torch.float32, "frequency", rows, dev),
+                    _opt(bias_ids, torch.int32, "bias_ids", (R, max_bias), dev),
+                    _opt(bias, torch.float32, "bias", (R, max_bias), dev), mask_ptr, mask_stride, max_hist, max_bias)
     if R == 0 or V == 0:   # empty tensors have no address
         return out
-    _device_call(lib().logits_process, "logits_process", dev, ctypes.addressof(c), logits.data_ptr(),
-                 logits.stride(0), _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0), _ptr(status))
+    _device_call(lib().logits_process, "logits_process", dev, c, logits.data_ptr(), logits.stride(0) if R > 1 else V,
+                 _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0) if R > 1 else V, _status(status, dev))
     return out
 
 
