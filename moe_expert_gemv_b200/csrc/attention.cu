@@ -74,7 +74,7 @@ struct AmLayout {
     static constexpr int off_off = st_off + S * 2 * tile;
     static constexpr int ml_off = off_off + S * AM_KT * 8;
     static constexpr int misc_off = ml_off + 2 * WK * M * 4;
-    static constexpr int total = misc_off + 128;
+    static constexpr int total = misc_off + 16;
     static_assert(WK * M * OP * 4 <= S * 2 * tile, "joined sums fit the ring");
 };
 
@@ -90,13 +90,12 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
     long long *off = reinterpret_cast<long long *>(smem + L::off_off);
     float *ml = reinterpret_cast<float *>(smem + L::ml_off);
     int *flag = reinterpret_cast<int *>(smem + L::misc_off);            // [0] last arrival, [1] V not finite
-    long long *scan = reinterpret_cast<long long *>(smem + L::misc_off + 16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int wr = warp / WK, wk = warp % WK;
     const int g = lane >> 2, tg = lane & 3;
 
     AttnWalk<M, AM_KT> w;
-    w.start(a, attn_span<M, AM_KT, AM_THREADS>(a, scan));
+    w.start(a, attn_span<M, AM_KT>(a));
     const float sc2 = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : a.scale * kLog2e;
     const float cap = a.softcap * kLog2e;
 

@@ -42,9 +42,9 @@ struct TcCfg {
     static constexpr int KS = 2, VS = 2;                 // stages; S buffers: also 2, row tiles or tiles in turn
     static constexpr int tile = KT * DP * 2;
     static constexpr int SOFT = 128 * NROW;              // softmax threads
-    static constexpr int LOAD = 96;                      // cp.async threads
-    static constexpr int FIX = 64;                       // beside the TMA warp
-    static constexpr int THREADS = SOFT + 128;
+    static constexpr int LOAD = 128;                     // loader threads
+    // beside them a warpgroup of the MMA warp, the K and the V warp of TMA
+    static constexpr int THREADS = SOFT + 128 + LOAD;
     // tensor memory columns
     static constexpr int s_col = 0;                      // + 128 per buffer
     static constexpr int o_col = 256;                    // + DP per row tile
@@ -54,7 +54,9 @@ struct TcCfg {
     static constexpr int off_off = v_off + VS * tile;    // [2][KT] int64
     static constexpr int bar_off = off_off + 2 * KT * 8;
     static constexpr int misc_off = bar_off + 32 * 8;
-    static constexpr int total = misc_off + 256 + 1024;  // + alignment slack
+    static constexpr int stg_off = misc_off + 64;        // 2 KB per softmax warp
+    static constexpr int total = stg_off + SOFT / 32 * 2048 + 1024;   // + alignment slack
+    static_assert(KT <= LOAD, "a loader thread per key");
     static_assert(o_col + NROW * DP <= 512, "tensor memory");
     static_assert(total <= 227 * 1024, "shared memory");
 };
@@ -97,6 +99,13 @@ __device__ __forceinline__ void at_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+// true for one thread of a converged warp, the same one each time
+__device__ __forceinline__ bool at_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void at_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -104,12 +113,6 @@ __device__ __forceinline__ void at_commit(uint64_t *bar)
 }
 __device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void at_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-#define AT_R32(v, o)                                                                                              \
-    v[o], v[o + 1], v[o + 2], v[o + 3], v[o + 4], v[o + 5], v[o + 6], v[o + 7], v[o + 8], v[o + 9], v[o + 10],    \
-        v[o + 11], v[o + 12], v[o + 13], v[o + 14], v[o + 15], v[o + 16], v[o + 17], v[o + 18], v[o + 19],        \
-        v[o + 20], v[o + 21], v[o + 22], v[o + 23], v[o + 24], v[o + 25], v[o + 26], v[o + 27], v[o + 28],        \
-        v[o + 29], v[o + 30], v[o + 31]
 
 // 32 lanes x 32 consecutive columns of tensor memory, without the wait
 __device__ __forceinline__ void at_ld32(uint32_t taddr, uint32_t *r)
@@ -134,7 +137,28 @@ __device__ __forceinline__ void at_st32(uint32_t taddr, const uint32_t *r)
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void at_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// The loads into r have landed.  The registers are operands, so that nothing
+// that uses them can be moved before the wait.
+__device__ __forceinline__ void at_wait_ld(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void at_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // bounded wait that gives up at once after another thread of the CTA did
@@ -209,20 +233,19 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     volatile int *abort_word = reinterpret_cast<volatile int *>(smem + C::misc_off + 4);
     volatile int *poison = reinterpret_cast<volatile int *>(smem + C::misc_off + 16);   // [4], by unit
     volatile int *armed_v = reinterpret_cast<volatile int *>(smem + C::misc_off + 32);  // [2], tile in the V stage
-    long long *scan = reinterpret_cast<long long *>(smem + C::misc_off + 64);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int W_MMA = C::SOFT / 32;
 
     if (tid == 0) {
         tc_shared<M, DP>(a)[blockIdx.x].c1 = 0;
         const int full = a.tma ? 1 : C::LOAD;
-        mbar_init(&bar[TB_QF], a.tma ? C::FIX : C::LOAD);
+        mbar_init(&bar[TB_QF], C::LOAD);
         mbar_init(&bar[TB_QE], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[TB_KF + i], full);
             mbar_init(&bar[TB_KE + i], 1);
             mbar_init(&bar[TB_VF + i], full);
-            mbar_init(&bar[TB_VX + i], C::FIX);
+            mbar_init(&bar[TB_VX + i], C::LOAD);
             mbar_init(&bar[TB_VE + i], 1);
             mbar_init(&bar[TB_SF + i], 1);
             mbar_init(&bar[TB_PF + i], 128);
@@ -242,7 +265,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_trigger();   // the joining kernel may be launched; it waits for this one's end
-    const AttnSpan span = attn_span<M, KT, C::THREADS>(a, scan);
+    const AttnSpan span = attn_span<M, KT>(a);
     at_fence_before();
     __syncthreads();
     at_fence_after();
@@ -251,106 +274,131 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     w.start(a, span);
 
     if (warp >= W_MMA) {
-        if (NROW == 2)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == W_MMA) {
             // ================================================= MMA issuer
-            if (lane == 0) {
-                const uint32_t idesc_s = at_idesc<T>(KT, false);
-                const int n_o = (a.dim + 15) & ~15, ksteps = (a.dim + 15) / 16;
-                const uint32_t idesc_o = at_idesc<T>(n_o, true);
-                const uint32_t qb = smem_u32(smem + C::q_off), kb = smem_u32(smem + C::k_off),
-                               vb = smem_u32(smem + C::v_off);
-                uint32_t kc = 0, vc = 0, un = 0;          // tiles and units so far
-                uint32_t pc[2] = {0, 0}, oc[2] = {0, 0}, xc[2] = {0, 0};
-                bool ok = true, issued = false;
-                auto wait = [&](int b, uint32_t parity) {
-                    ok = ok && at_wait(&bar[b], parity & 1, a.status, abort_word);
-                    return ok;
-                };
-                auto scores = [&](int buf, int rt, uint32_t ks) {
-                    const uint32_t q = qb + rt * 128 * 128, k = kb + ks * C::tile;
-                    for (int i = 0; i < ksteps; ++i)
-                        at_mma_ss(tmem + C::s_col + buf * 128,
-                                  at_desc(q + (i >> 2) * M * 128 + (i & 3) * 32, 16),
-                                  at_desc(k + (i >> 2) * KT * 128 + (i & 3) * 32, 16), idesc_s, i > 0);
-                    at_commit(&bar[TB_SF + buf]);
-                    issued = true;
-                };
-                auto values = [&](int buf, int rt, uint32_t vs, bool acc) {
-                    const uint32_t v = vb + vs * C::tile;
-                    for (int i = 0; i < KT / 16; ++i)
-                        at_mma_ts(tmem + C::o_col + rt * DP, tmem + C::s_col + buf * 128 + i * 8,
-                                  at_desc(v + i * 2048, KT * 128), idesc_o, acc || i > 0);
-                };
-                for (; !w.done() && ok; w.next(a), ++un) {
-                    const int nt = w.tb() - w.ta();
-                    const int rows = min(M, w.s.n * a.group - w.rt * M);
-                    const int nr = NROW == 2 && rows > 128 ? 2 : 1;   // row tiles with rows
-                    int lo_max, hi_min;
-                    at_limits(a, w.s, w.rt * M, rows, lo_max, hi_min);
-                    if (!wait(TB_QF, un) || !wait(TB_KF + kc % 2, kc / 2))
-                        break;
-                    at_fence_after();
-                    for (int r = 0; r < nr; ++r)
-                        scores(NROW == 2 ? r : 0, r, kc % 2);
-                    at_commit(&bar[TB_KE + kc % 2]);
-                    ++kc;
-                    if (nt == 1)
-                        at_commit(&bar[TB_QE]);
-                    for (int j = 0; j < nt && ok; ++j, ++vc) {
-                        const bool more = j + 1 < nt;
-                        if (NROW == 1 && more) {
-                            if (!wait(TB_KF + kc % 2, kc / 2))
-                                break;
-                            at_fence_after();
-                            scores((j + 1) & 1, 0, kc % 2);
-                            at_commit(&bar[TB_KE + kc % 2]);
-                            ++kc;
-                            if (j + 2 == nt)
-                                at_commit(&bar[TB_QE]);
-                        }
-                        const int j0 = (w.t0 + w.ta() + j) * KT;
-                        if (a.tma && (j0 < lo_max || j0 + KT > hi_min)) {
-                            if (!wait(TB_VX + vc % 2, xc[vc % 2]))
-                                break;
-                            ++xc[vc % 2];
-                        } else if (!wait(TB_VF + vc % 2, vc / 2)) {
-                            break;
-                        }
-                        if (NROW == 2 && more && !wait(TB_KF + kc % 2, kc / 2))
-                            break;
-                        for (int r = 0; r < nr && ok; ++r) {
-                            const int buf = NROW == 2 ? r : j & 1;
-                            if (!wait(TB_PF + buf, pc[buf]))
-                                break;
-                            ++pc[buf];
-                            if (j == 0 && oc[r] > 0 && !wait(TB_OE + r, oc[r] - 1))
-                                break;   // the last unit's O has been read
-                            at_fence_after();
-                            values(buf, r, vc % 2, j > 0);
-                            if (NROW == 1)
-                                at_commit(&bar[TB_PV]);
-                            if (NROW == 2 && more)
-                                scores(buf, r, kc % 2);
-                            if (!more) {
-                                at_commit(&bar[TB_OF + r]);
-                                ++oc[r];
-                            }
-                        }
-                        at_commit(&bar[TB_VE + vc % 2]);
-                        if (NROW == 2 && more) {
-                            at_commit(&bar[TB_KE + kc % 2]);
-                            ++kc;
-                            if (j + 2 == nt)
-                                at_commit(&bar[TB_QE]);
-                        }
+            // The whole warp walks and waits; one elected thread issues.
+            const uint32_t idesc_s = at_idesc<T>(KT, false);
+            const int n_o = (a.dim + 15) & ~15, ksteps = (a.dim + 15) / 16;
+            const uint32_t idesc_o = at_idesc<T>(n_o, true);
+            const uint64_t qd = at_desc(smem_u32(smem + C::q_off), 16), kd = at_desc(smem_u32(smem + C::k_off), 16),
+                           vd = at_desc(smem_u32(smem + C::v_off), KT * 128);
+            uint32_t kc = 0, vc = 0, un = 0;          // tiles and units so far
+            uint32_t pc[2] = {0, 0}, oc[2] = {0, 0}, xc[2] = {0, 0};
+            bool ok = true, issued = false;
+            auto wait = [&](int b, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, at_wait(&bar[b], parity & 1, a.status, abort_word));
+                return ok;
+            };
+            auto commit = [&](int b) {
+                if (at_elect())
+                    at_commit(&bar[b]);
+                __syncwarp();
+            };
+            // Products are issued from straight code, the descriptors' start
+            // addresses (in units of 16 bytes) stepped by constants: built anew
+            // for each step, they took the thread longer than the 64 cycles that
+            // the step takes.
+            auto scores = [&](int buf, int rt, uint32_t ks) {
+                const uint64_t q = qd + rt * (128 * 128 / 16), k = kd + ks * (C::tile / 16);
+                const uint32_t d = tmem + C::s_col + buf * 128;
+                if (ksteps == DP / 16) {
+                    if (at_elect()) {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i)
+                            at_mma_ss(d, q + ((i >> 2) * M * 128 + (i & 3) * 32) / 16,
+                                      k + ((i >> 2) * KT * 128 + (i & 3) * 32) / 16, idesc_s, i > 0);
+                    }
+                } else {
+                    if (at_elect()) {
+#pragma unroll 1
+                        for (int i = 0; i < ksteps; ++i)
+                            at_mma_ss(d, q + ((i >> 2) * M * 128 + (i & 3) * 32) / 16,
+                                      k + ((i >> 2) * KT * 128 + (i & 3) * 32) / 16, idesc_s, i > 0);
                     }
                 }
-                if (issued) {   // nothing is in flight when the tensor memory is freed
-                    at_commit(&bar[TB_DRAIN]);
-                    mbar_wait(&bar[TB_DRAIN], 0, a.status);
+                __syncwarp();
+                commit(TB_SF + buf);
+                issued = true;
+            };
+            auto values = [&](int buf, int rt, uint32_t vs, bool acc) {
+                const uint64_t v = vd + vs * (C::tile / 16);
+                const uint32_t d = tmem + C::o_col + rt * DP, p = tmem + C::s_col + buf * 128;
+                if (at_elect()) {
+#pragma unroll
+                    for (int i = 0; i < KT / 16; ++i)
+                        at_mma_ts(d, p + i * 8, v + i * 128, idesc_o, i > 0 || acc);
                 }
+                __syncwarp();
+            };
+            for (; !w.done() && ok; w.next(a), ++un) {
+                const int nt = w.tb() - w.ta();
+                const int rows = min(M, w.s.n * a.group - w.rt * M);
+                const int nr = NROW == 2 && rows > 128 ? 2 : 1;   // row tiles with rows
+                int lo_max, hi_min;
+                at_limits(a, w.s, w.rt * M, rows, lo_max, hi_min);
+                if (!wait(TB_QF, un) || !wait(TB_KF + kc % 2, kc / 2))
+                    break;
+                at_fence_after();
+                for (int r = 0; r < nr; ++r)
+                    scores(NROW == 2 ? r : 0, r, kc % 2);
+                commit(TB_KE + kc % 2);
+                ++kc;
+                if (nt == 1)
+                    commit(TB_QE);
+                for (int j = 0; j < nt && ok; ++j, ++vc) {
+                    const bool more = j + 1 < nt;
+                    if (NROW == 1 && more) {
+                        if (!wait(TB_KF + kc % 2, kc / 2))
+                            break;
+                        at_fence_after();
+                        scores((j + 1) & 1, 0, kc % 2);
+                        commit(TB_KE + kc % 2);
+                        ++kc;
+                        if (j + 2 == nt)
+                            commit(TB_QE);
+                    }
+                    const int j0 = (w.t0 + w.ta() + j) * KT;
+                    if (a.tma && (j0 < lo_max || j0 + KT > hi_min)) {
+                        if (!wait(TB_VX + vc % 2, xc[vc % 2]))
+                            break;
+                        ++xc[vc % 2];
+                    } else if (!wait(TB_VF + vc % 2, vc / 2)) {
+                        break;
+                    }
+                    if (NROW == 2 && more && !wait(TB_KF + kc % 2, kc / 2))
+                        break;
+                    for (int r = 0; r < nr; ++r) {
+                        const int buf = NROW == 2 ? r : j & 1;
+                        if (!wait(TB_PF + buf, pc[buf]))
+                            break;
+                        ++pc[buf];
+                        if (j == 0 && oc[r] > 0 && !wait(TB_OE + r, oc[r] - 1))
+                            break;   // the last unit's O has been read
+                        at_fence_after();
+                        values(buf, r, vc % 2, j > 0);
+                        if (NROW == 1)
+                            commit(TB_PV);
+                        if (NROW == 2 && more)
+                            scores(buf, r, kc % 2);
+                        if (!more) {
+                            commit(TB_OF + r);
+                            ++oc[r];
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    commit(TB_VE + vc % 2);
+                    if (NROW == 2 && more) {
+                        commit(TB_KE + kc % 2);
+                        ++kc;
+                        if (j + 2 == nt)
+                            commit(TB_QE);
+                    }
+                }
+            }
+            if (issued) {   // nothing is in flight when the tensor memory is freed
+                commit(TB_DRAIN);
+                mbar_wait(&bar[TB_DRAIN], 0, a.status);
             }
             __syncwarp();
         } else {
@@ -412,71 +460,76 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
-            if (a.tma && warp == W_MMA + 1) {
-                // ---- TMA: each lane a box of the tile's keys
-                const int nbox = KT / a.tma, nblk = (a.dim + 63) / 64;
+            if (warp < W_MMA + 4) {
+                // ---- TMA: one warp for K, one for V (so that K never waits for
+                // a slot of V), each lane a box of the tile's keys
+                const int x = warp - W_MMA - 1;
+                const int nbox = KT / max(a.tma, 1), nblk = (a.dim + 63) / 64;
                 const uint32_t bytes = KT * 128 * nblk;
-                uint32_t n = 0, armed[2] = {0, 0};   // tiles so far, copies of K and V
-                if (lane == 0) {
-                    prefetch_tensormap(&maps.k);
-                    prefetch_tensormap(&maps.v);
-                }
-                for (; !w.done() && !dead; w.next(a)) {
+                const void *map = x ? &maps.v : &maps.k;
+                uint32_t n = 0;   // tiles so far
+                if (lane == 0)
+                    prefetch_tensormap(map);
+                for (; a.tma && x < 2 && !w.done() && !dead; w.next(a)) {
                     const int ta = w.ta(), tb = w.tb();
-                    long long box = lane < nbox ? attn_box(a, w.sp.b, (w.t0 + ta) * KT + lane * a.tma, w.lo, w.hi) : 0;
-                    for (int t = ta; t < tb && !dead; ++t, ++n) {
-                        const int page = (int)(box >> 32), slot = (int)(box & 0xFFFFFFFFll);
+                    int j = (w.t0 + ta) * KT + lane * a.tma;
+                    int ahead = lane < nbox ? attn_page(a, w.sp.b, j, w.lo, w.hi) : 0;
+                    for (int t = ta; t < tb; ++t, ++n, j += KT) {
+                        int page = ahead;
+                        const int slot = (int)((unsigned)j % (unsigned)a.page_size);
                         if (t + 1 < tb && lane < nbox)   // on its way while this tile's copies go out
-                            box = attn_box(a, w.sp.b, (w.t0 + t + 1) * KT + lane * a.tma, w.lo, w.hi);
-                        for (int x = 0; x < 2 && !dead; ++x) {   // K, then V
-                            uint64_t *full = &bar[(x ? TB_VF : TB_KF) + n % 2];
-                            if (n >= 2 && !__all_sync(0xffffffffu, at_wait(&bar[(x ? TB_VE : TB_KE) + n % 2],
-                                                                           (n / 2 - 1) & 1, a.status, abort_word))) {
-                                dead = true;
-                                break;
+                            ahead = attn_page(a, w.sp.b, j + KT, w.lo, w.hi);
+                        if (n >= 2 && !__all_sync(0xffffffffu, at_wait(&bar[(x ? TB_VE : TB_KE) + n % 2], (n / 2 - 1) & 1,
+                                                                       a.status, abort_word))) {
+                            dead = true;
+                            break;
+                        }
+                        uint64_t *full = &bar[(x ? TB_VF : TB_KF) + n % 2];
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, bytes);
+                            if (x)
+                                armed_v[n % 2] = (int)n;
+                        }
+                        __syncwarp();
+                        if (lane < nbox) {
+                            if ((unsigned)page > (unsigned)a.num_pages ||
+                                (page == a.num_pages && j < w.hi && j + a.tma > w.lo)) {
+                                flag_status(a.status, QMOE_DEV_BAD_PAGE);
+                                page = a.num_pages;
                             }
-                            if (lane == 0) {
-                                mbar_arrive_expect_tx(full, bytes);
-                                if (x == 1)
-                                    armed_v[n % 2] = (int)n;
-                            }
-                            ++armed[x];
-                            __syncwarp();
                             const uint32_t dst = smem_u32(smem + (x ? C::v_off : C::k_off) + (n % 2) * C::tile) +
                                                  lane * a.tma * 128;
-                            if (lane < nbox)
-                                for (int k = 0; k < nblk; ++k)
-                                    tma_load_4d(dst + k * KT * 128, x ? &maps.v : &maps.k, k * 64,
-                                                a.heads_inner ? w.h : slot, a.heads_inner ? slot : w.h, page, full);
-                            __syncwarp();
+                            for (int k = 0; k < nblk; ++k)
+                                tma_load_4d(dst + k * KT * 128, map, k * 64, a.heads_inner ? w.h : slot,
+                                            a.heads_inner ? slot : w.h, page, full);
                         }
+                        __syncwarp();
                     }
                 }
                 // no copy may still be landing when the CTA exits
                 if (lane == 0)
-                    for (int x = 0; x < 2; ++x)
-                        for (uint32_t i = armed[x] > 2 ? armed[x] - 2 : 0; i < armed[x]; ++i)
-                            mbar_wait(&bar[(x ? TB_VF : TB_KF) + i % 2], (i / 2) & 1, a.status);
+                    for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i)
+                        mbar_wait(&bar[(x ? TB_VF : TB_KF) + i % 2], (i / 2) & 1, a.status);
                 __syncwarp();
             } else if (a.tma) {
                 // ---- beside it: the query rows, and V at the limits
-                const int t = tid - C::SOFT - 64;
+                const int t = tid - C::SOFT - 128;
                 uint32_t un = 0, n = 0;
                 for (; !w.done(); w.next(a), ++un) {
                     const int ta = w.ta(), tb = w.tb();
                     const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
                     if (un > 0 && !at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))
                         dead = true;
-                    if (bar_any(TC_BAR_LOAD, C::FIX, dead))
+                    if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
                         break;
                     if (t == 0)
                         poison[un & 3] = 0;
-                    load_q(t, C::FIX, row0, rows);
+                    load_q(t, C::LOAD, row0, rows);
                     cp_async_commit();
                     cp_async_wait<0>();
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(&bar[TB_QF]);
-                    named_bar_sync(TC_BAR_LOAD, C::FIX);   // the cleared poison flag is seen
+                    named_bar_sync(TC_BAR_LOAD, C::LOAD);   // the cleared poison flag is seen
                     int lo_max, hi_min;
                     at_limits(a, w.s, row0, rows, lo_max, hi_min);
                     for (int i = ta; i < tb && !dead; ++i) {
@@ -491,14 +544,14 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                             dead = true;
                             break;
                         }
-                        clean_v(s % 2, j0, lo_max, hi_min, un, t, C::FIX);
+                        clean_v(s % 2, j0, lo_max, hi_min, un, t, C::LOAD);
                         mbar_arrive(&bar[TB_VX + s % 2]);
                     }
                     n += tb - ta;
                 }
             } else {
                 // ---- cp.async
-                const int lt = tid - C::SOFT - 32;
+                const int lt = tid - C::SOFT - 128;
                 long long *off = reinterpret_cast<long long *>(smem + C::off_off);
                 uint32_t kc = 0, un = 0;
                 // copies in flight, oldest first: the barrier to arrive at and, for
@@ -556,7 +609,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 for (; !w.done(); w.next(a), ++un) {
                     const int ta = w.ta(), tb = w.tb();
                     const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
-                    long long o0 = slot(ta, tb, lt), o1 = slot(ta, tb, lt + C::LOAD);
+                    long long o0 = slot(ta, tb, lt);
                     acquire(TB_QE, un, 1);
                     at_limits(a, w.s, row0, rows, lo_max, hi_min);
                     if (bar_any(TC_BAR_LOAD, C::LOAD, dead || *abort_word != 0))
@@ -569,13 +622,10 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         long long *o = off + (t & 1) * KT;
                         if (lt < KT)
                             o[lt] = o0;
-                        if (lt + C::LOAD < KT)
-                            o[lt + C::LOAD] = o1;
                         // (the barrier also keeps the loaders together after a timeout)
                         if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
                             break;
                         o0 = slot(t + 1, tb, lt);
-                        o1 = slot(t + 1, tb, lt + C::LOAD);
                         for (int x = 0; x < 2; ++x) {   // K, then V
                             const int fb = (x ? TB_VF : TB_KF) + (int)(kc % 2);
                             acquire((x ? TB_VE : TB_KE) + (int)(kc % 2), kc, 2);
@@ -617,8 +667,6 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
         }
     } else {
         // ====================================================== softmax
-        if (NROW == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int rt = warp >> 2, quad = warp & 3;
         const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
         const int rr = rt * 128 + quad * 32 + lane;   // row of the unit
@@ -646,28 +694,43 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     ++sc[buf];
                     at_fence_after();
                     const uint32_t ts = tq + C::s_col + buf * 128;
-                    uint32_t s[KT];
-#pragma unroll
-                    for (int c = 0; c < KT; c += 32)
-                        at_ld32(ts + c, s + c);
-                    at_wait_ld();
                     const int j0 = (w.t0 + t) * KT;
-                    if (a.softcap > 0.f) {
-#pragma unroll
-                        for (int c = 0; c < KT; ++c)
-                            s[c] = __float_as_uint(capped(__uint_as_float(s[c]), capc, cap));
-                    }
                     const int l0 = lo - j0, h0 = hi - j0;
-                    if (__any_sync(0xffffffffu, l0 > 0 || h0 < KT)) {
-#pragma unroll
-                        for (int c = 0; c < KT; ++c)
-                            if (c < l0 || c >= h0)
-                                s[c] = 0xFF800000u;   // -inf
-                    }
+                    const bool cut = __any_sync(0xffffffffu, l0 > 0 || h0 < KT);
+                    // first pass: the maximum (32 columns at a time, the next ones
+                    // on their way: all 128 at once would not leave the registers
+                    // of 512 threads); caps and masks go back to tensor memory
+                    uint32_t s[2][32];
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    at_ld32(ts, s[0]);
 #pragma unroll
-                    for (int c = 0; c < KT; ++c)
-                        mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+                    for (int c = 0; c < KT / 32; ++c) {
+                        uint32_t *x = s[c & 1];
+                        at_wait_ld(x);
+                        if (c + 1 < KT / 32)
+                            at_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+                        if (a.softcap > 0.f || cut) {
+                            if (a.softcap > 0.f) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    x[i] = __float_as_uint(capped(__uint_as_float(x[i]), capc, cap));
+                            }
+                            if (cut) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (32 * c + i < l0 || 32 * c + i >= h0)
+                                        x[i] = 0xFF800000u;   // -inf
+                            }
+                            at_st32(ts + 32 * c, x);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            mx[(i >> 1) & 3] =
+                                fmaxf(fmaxf(mx[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                    }
+                    if (a.softcap > 0.f || cut)
+                        at_wait_st();
+                    at_ld32(ts, s[0]);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc2;
                     const bool grow = top > m + TC_LAZY || (m == -INFINITY && top > m);
                     if (__any_sync(0xffffffffu, grow)) {
@@ -687,7 +750,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                             for (int c = 0; c < a.dim; c += 32) {
                                 uint32_t v[32];
                                 at_ld32(to + c, v);
-                                at_wait_ld();
+                                at_wait_ld(v);
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
                                     v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
@@ -696,21 +759,26 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
+                    // second pass: the weights, over the scores already read
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < KT; c += 64) {
-                        uint32_t p[32];
+                    for (int c = 0; c < KT / 32; ++c) {
+                        uint32_t *x = s[c & 1];
+                        at_wait_ld(x);
+                        if (c + 1 < KT / 32)
+                            at_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+                        uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float x = exp2_approx(fmaf(__uint_as_float(s[c + 2 * i]), sc2, -base));
-                            const float y = exp2_approx(fmaf(__uint_as_float(s[c + 2 * i + 1]), sc2, -base));
-                            sum[(2 * i) & 3] += x;
-                            sum[(2 * i + 1) & 3] += y;
+                        for (int i = 0; i < 16; ++i) {
+                            const float u = exp2_approx(fmaf(__uint_as_float(x[2 * i]), sc2, -base));
+                            const float v = exp2_approx(fmaf(__uint_as_float(x[2 * i + 1]), sc2, -base));
+                            sum[(2 * i) & 3] += u;
+                            sum[(2 * i + 1) & 3] += v;
                             // the weights enter the product in the cache's type (at
                             // most half a step each); their sum stays unrounded
-                            p[i] = Num16<T>::down2(x, y);
+                            p[i] = Num16<T>::down2(u, v);
                         }
-                        at_st32(ts + c / 2, p);
+                        at_st16(ts + 16 * c, p);
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     at_wait_st();
@@ -731,49 +799,76 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     int lo_max = 0, hi_min = 0;
                     if (bad)
                         at_limits(a, w.s, row0, rows, lo_max, hi_min);
-                    for (int c = 0; c < a.dim; c += 32) {
+                    // 16 rows x 128 bytes at a time through shared memory, so that
+                    // 8 lanes write a row's 128 bytes together
+                    unsigned char *stg = smem + C::stg_off + warp * 2048;
+                    const int step = whole ? 64 : 32;   // columns of 128 bytes
+                    for (int c0 = 0; c0 < a.dim; c0 += step) {
                         uint32_t v[32];
-                        at_ld32(to + c, v);
-                        at_wait_ld();
-                        if (rr >= rows)
-                            continue;
-                        if (bad) {   // the values taken out by the loaders, for the rows that see them
-                            const int j1 = min(hi, (w.t0 + tb) * KT);
-                            for (int j = max(lo, (w.t0 + ta) * KT); j < j1; ++j) {
-                                if (j >= lo_max && j < hi_min) {
-                                    j = hi_min - 1;
-                                    continue;
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int c = c0 + 32 * half;
+                            if (half && (!whole || c >= a.dim))
+                                break;
+                            uint32_t u[32];
+                            at_ld32(to + c, u);
+                            at_wait_ld(u);
+                            if (bad && rr < rows) {   // the values taken out by the loaders, for the rows that see them
+                                const int j1 = min(hi, (w.t0 + tb) * KT);
+                                for (int j = max(lo, (w.t0 + ta) * KT); j < j1; ++j) {
+                                    if (j >= lo_max && j < hi_min) {
+                                        j = hi_min - 1;
+                                        continue;
+                                    }
+                                    const long long e = attn_slot(a, w.sp.b, w.h, j);
+                                    if (e < 0)
+                                        continue;
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i)
+                                        if (c + i < a.dim) {
+                                            const float x = Num16<T>::up(a.v[e + c + i]);
+                                            if (!isfinite(x))
+                                                u[i] = __float_as_uint(__uint_as_float(u[i]) + x);
+                                        }
                                 }
-                                const long long e = attn_slot(a, w.sp.b, w.h, j);
-                                if (e < 0)
-                                    continue;
+                            }
+                            if (whole) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    v[16 * half + i] = Num16<T>::down2(__uint_as_float(u[2 * i]) * inv,
+                                                                       __uint_as_float(u[2 * i + 1]) * inv);
+                            } else {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    if (c + i < a.dim) {
-                                        const float x = Num16<T>::up(a.v[e + c + i]);
-                                        if (!isfinite(x))
-                                            v[i] = __float_as_uint(__uint_as_float(v[i]) + x);
-                                    }
+                                    v[i] = u[i];
                             }
                         }
-                        if (whole) {
-                            uint16_t *dst = a.out + (w.s.q0 + tok) * a.o_token + hq * a.o_head + c;
 #pragma unroll
-                            for (int i = 0; i < 32; i += 8)
-                                if (c + i < a.dim) {
-                                    uint4 u;
-                                    u.x = Num16<T>::down2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
-                                    u.y = Num16<T>::down2(__uint_as_float(v[i + 2]) * inv, __uint_as_float(v[i + 3]) * inv);
-                                    u.z = Num16<T>::down2(__uint_as_float(v[i + 4]) * inv, __uint_as_float(v[i + 5]) * inv);
-                                    u.w = Num16<T>::down2(__uint_as_float(v[i + 6]) * inv, __uint_as_float(v[i + 7]) * inv);
-                                    *reinterpret_cast<uint4 *>(dst + i) = u;
+                        for (int part16 = 0; part16 < 2; ++part16) {
+                            __syncwarp();
+                            if ((lane >> 4) == part16) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<uint4 *>(stg + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = i * 4 + (lane >> 3), row = rt * 128 + quad * 32 + part16 * 16 + r;
+                                const int u = lane & 7;
+                                const uint4 x = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((u ^ (r & 7)) << 4));
+                                if (row >= rows || c0 + u * (step / 8) >= a.dim)
+                                    continue;
+                                if (whole) {
+                                    const int tk = (row0 + row) / a.group;
+                                    const int hd = w.h * a.group + (row0 + row) - tk * a.group;
+                                    *reinterpret_cast<uint4 *>(a.out + (w.s.q0 + tk) * a.o_token + hd * a.o_head + c0 +
+                                                               u * 8) = x;
+                                } else {
+                                    *reinterpret_cast<uint4 *>(part + (size_t)row * DP + c0 + u * 4) = x;
                                 }
-                        } else {
-                            float *dst = part + (size_t)rr * DP + c;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                if (c + i < a.dim)
-                                    *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            }
                         }
                     }
                     at_fence_before();

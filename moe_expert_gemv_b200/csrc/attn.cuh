@@ -148,32 +148,6 @@ __device__ __forceinline__ long long attn_seq_tiles(const AttnArgs &a, const Att
     return w * a.kv_heads;
 }
 
-// Inclusive sum of v over the first NT threads' lanes; sm: NT/32 words.
-template <int NT>
-__device__ __forceinline__ long long block_scan(long long v, long long *sm, long long &total)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o)
-            v += u;
-    }
-    if (lane == 31)
-        sm[warp] = v;
-    __syncthreads();
-    long long before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp)
-            before += sm[w];
-        total += sm[w];
-    }
-    __syncthreads();
-    return v + before;
-}
-
 // This CTA's interval [x, end) of the line of tiles, and the sequence that
 // holds tile x with the line's index of its first tile.
 struct AttnSpan {
@@ -182,47 +156,51 @@ struct AttnSpan {
     int ctas;   // CTAs with work: each has at least one tile
 };
 
-// all NT threads of the CTA; sm: NT/32 + 2 words of shared memory
-template <int M, int KT, int NT>
-__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a, long long *sm)
+// Every warp works it out by itself, a lane a sequence: no block barrier, and
+// the lengths are read once (from L1 by the later warps).
+template <int M, int KT>
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
 {
+    const int lane = threadIdx.x & 31;
     AttnSpan sp;
-    long long total = 0, mine = 0, incl = 0, sum;
-    for (int b0 = 0; b0 < a.batch; b0 += NT) {
-        const int b = b0 + (int)threadIdx.x;
-        mine = b < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b)) : 0;
-        if (blockIdx.x == 0 && b < a.batch && a.kv_len[b] > (long long)a.max_pages * a.page_size)
+    long long mine = 0, sum = 0;
+    for (int b = lane; b < a.batch; b += 32) {
+        if (blockIdx.x == 0 && threadIdx.x < 32 && a.kv_len[b] > (long long)a.max_pages * a.page_size)
             flag_status(a.status, QMOE_DEV_BAD_PAGE);
-        incl = block_scan<NT>(mine, sm, sum);
-        total += sum;
+        mine = attn_seq_tiles<M, KT>(a, attn_seq(a, b));
+        sum += mine;
     }
-    sp.total = total;
-    sp.ctas = (int)min(total, (long long)gridDim.x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    sp.total = sum;
+    sp.ctas = (int)min(sum, (long long)gridDim.x);
     const long long c = min((int)blockIdx.x, sp.ctas);
-    sp.x = sp.ctas ? total * c / sp.ctas : 0;
-    sp.end = c < sp.ctas ? total * (c + 1) / sp.ctas : sp.x;
+    sp.x = sp.ctas ? sum * c / sp.ctas : 0;
+    sp.end = c < sp.ctas ? sum * (c + 1) / sp.ctas : sp.x;
+    sp.first = 0;
+    sp.b = 0;
     if (sp.x >= sp.end)
         return sp;
-    long long before = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += NT) {
-        if (a.batch > NT) {
-            const int b = b0 + (int)threadIdx.x;
-            mine = b < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b)) : 0;
-            incl = block_scan<NT>(mine, sm, sum);
-        } else {
-            sum = total;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        if (a.batch > 32)
+            mine = b0 + lane < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b0 + lane)) : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += u;
         }
-        if (before + incl - mine <= sp.x && sp.x < before + incl) {
-            sm[NT / 32] = before + incl - mine;
-            sm[NT / 32 + 1] = b0 + (int)threadIdx.x;
-        }
-        before += sum;
-        if (before > sp.x)
+        const unsigned holds = __ballot_sync(0xffffffffu, sp.first + incl > sp.x);
+        if (holds) {
+            const int l = __ffs(holds) - 1;
+            sp.b = b0 + l;
+            sp.first += __shfl_sync(0xffffffffu, incl - mine, l);
             break;
+        }
+        sp.first += __shfl_sync(0xffffffffu, incl, 31);
     }
-    __syncthreads();
-    sp.first = sm[NT / 32];
-    sp.b = (int)sm[NT / 32 + 1];
     return sp;
 }
 
@@ -340,21 +318,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c
         : "memory");
 }
 
-// keys [j, j + a.tma) of sequence b: where they lie, packed as page << 32 |
-// slot; page a.num_pages (beyond the cache: the copy writes zeros) where the
-// unit reads none of them or the page id is bad
-__device__ __forceinline__ long long attn_box(const AttnArgs &a, int b, int j, int lo, int hi)
+// The page that holds the box of keys [j, j + a.tma) of sequence b, as the
+// table says, or a.num_pages (beyond the cache: the copy writes zeros) where
+// the unit reads none of them.
+__device__ __forceinline__ int attn_page(const AttnArgs &a, int b, int j, int lo, int hi)
 {
-    const int pg = (int)((unsigned)j / (unsigned)a.page_size);
-    int id = a.num_pages;
-    if (j < hi && j + a.tma > lo) {
-        id = __ldg(a.table + (size_t)b * a.max_pages + pg);
-        if ((unsigned)id >= (unsigned)a.num_pages) {
-            flag_status(a.status, QMOE_DEV_BAD_PAGE);
-            id = a.num_pages;
-        }
-    }
-    return ((long long)id << 32) | (uint32_t)(j - pg * a.page_size);
+    if (j >= hi || j + a.tma <= lo)
+        return a.num_pages;
+    return __ldg(a.table + (size_t)b * a.max_pages + (int)((unsigned)j / (unsigned)a.page_size));
 }
 
 // ----------------------------------------------------------------- joining --
