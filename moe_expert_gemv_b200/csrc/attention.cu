@@ -23,6 +23,7 @@ namespace {
 
 constexpr int AM_THREADS = 128;
 constexpr int AM_KT = 64;
+constexpr int AM_EX = 0;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -94,8 +95,8 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
     const int wr = warp / WK, wk = warp % WK;
     const int g = lane >> 2, tg = lane & 3;
 
-    AttnWalk<M, AM_KT> w;
-    w.start(a, attn_span<M, AM_KT>(a));
+    AttnWalk<M, AM_KT, AM_EX> w;
+    w.start(a, attn_span<M, AM_KT, AM_EX>(a));
     const float sc2 = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : a.scale * kLog2e;
     const float cap = a.softcap * kLog2e;
 
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
         }
         __syncthreads();
         const bool whole = ta == 0 && tb == w.nt;
-        const int c0 = attn_cta(w.sp, w.u0), c1 = attn_cta(w.sp, w.u0 + w.nt - 1);
+        const int c0 = w.c0(), c1 = w.c1();
         float *part = attn_part<M, DP>(a, blockIdx.x, ta == 0);
         const int d4 = a.dim / 4;
         for (int i = tid; i < rows * d4; i += AM_THREADS) {
@@ -404,20 +405,46 @@ cudaError_t launch_dim(const AttnArgs &a, long long max_rows, const LaunchCfg &c
 
 }  // namespace
 
-bool attn_maps(const AttnArgs &a, bool bf16, int kt, AttnMaps *m, int *rows, int *heads_inner)
-{
-    typedef CUresult (*Encode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+typedef CUresult (*AttnEncode)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode fn = []() -> Encode {
+
+static AttnEncode attn_encode()
+{
+    static const AttnEncode fn = []() -> AttnEncode {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<Encode>(p);
+            return reinterpret_cast<AttnEncode>(p);
         (void)cudaGetLastError();
         return nullptr;
     }();
+    return fn;
+}
+
+bool attn_q_map(const AttnArgs &a, bool bf16, CUtensorMap *m)
+{
+    const AttnEncode fn = attn_encode();
+    if (!fn || a.group > 128 || 128 % a.group || a.dim < 64)
+        return false;
+    const cuuint64_t head = a.heads > 1 ? 2 * a.q_head : 2 * a.dim;
+    const cuuint64_t tok = a.tokens > 1 ? 2 * a.q_token : head * a.heads;
+    if (head < 2 * (cuuint64_t)a.dim || head % 16 || tok < head || tok % head || tok >= (cuuint64_t)1 << 40)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.heads, (cuuint64_t)a.tokens};
+    const cuuint64_t strides[2] = {head, tok};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.group, (cuuint32_t)(128 / a.group)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<uint16_t *>(a.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool attn_maps(const AttnArgs &a, bool bf16, int kt, AttnMaps *m, int *rows, int *heads_inner)
+{
+    const AttnEncode fn = attn_encode();
     int r = kt;
     while (r > a.page_size || a.page_size % r)
         r /= 2;   // kt is a power of two

@@ -35,6 +35,8 @@ namespace {
 
 constexpr float TC_LAZY = 8.f;   // log2 of the growth of a maximum that O is not rescaled for
 
+constexpr int TC_EX = 3;         // beginning and ending a unit, in tiles
+
 template <int DP, int NROW>
 struct TcCfg {
     static constexpr int KT = DP == 256 ? 64 : 128;      // keys per tile
@@ -45,6 +47,8 @@ struct TcCfg {
     static constexpr int LOAD = 128;                     // loader threads
     // beside them a warpgroup of the MMA warp, the K and the V warp of TMA
     static constexpr int THREADS = SOFT + 128 + LOAD;
+    // registers a thread: the softmax holds a row's scores
+    static constexpr int R_SOFT = NROW == 2 ? 168 : 232, R_REST = NROW == 2 ? 88 : 128;
     // tensor memory columns
     static constexpr int s_col = 0;                      // + 128 per buffer
     static constexpr int o_col = 256;                    // + DP per row tile
@@ -54,8 +58,10 @@ struct TcCfg {
     static constexpr int off_off = v_off + VS * tile;    // [2][KT] int64
     static constexpr int bar_off = off_off + 2 * KT * 8;
     static constexpr int misc_off = bar_off + 32 * 8;
-    static constexpr int stg_off = misc_off + 64;        // 2 KB per softmax warp
-    static constexpr int total = stg_off + SOFT / 32 * 2048 + 1024;   // + alignment slack
+    static constexpr int walk_off = misc_off + 64;       // a warp's place in its interval
+    static constexpr int ml_off = walk_off + THREADS / 32 * 128;   // the rows' maxima and sums
+    static constexpr int stg_off = ml_off + M * 8;       // 2 KB per loader warp, which also write the output
+    static constexpr int total = stg_off + LOAD / 32 * 2048 + 1024;   // + alignment slack
     static_assert(KT <= LOAD, "a loader thread per key");
     static_assert(o_col + NROW * DP <= 512, "tensor memory");
     static_assert(total <= 227 * 1024, "shared memory");
@@ -63,10 +69,10 @@ struct TcCfg {
 
 enum {
     TB_QF = 0, TB_QE, TB_KF, TB_KE = TB_KF + 2, TB_VF = TB_KE + 2, TB_VE = TB_VF + 2, TB_SF = TB_VE + 2,
-    TB_PF = TB_SF + 2, TB_OF = TB_PF + 2, TB_OE = TB_OF + 2, TB_VX = TB_OE + 2, TB_PV = TB_VX + 2, TB_DRAIN, TB_COUNT
+    TB_PF = TB_SF + 2, TB_OF = TB_PF + 2, TB_OE = TB_OF + 2, TB_VX = TB_OE + 2, TB_P2 = TB_VX + 2, TB_LF = TB_P2 + 2, TB_PV = TB_LF + 2, TB_DRAIN, TB_COUNT
 };
 static_assert(TB_COUNT <= 32, "barriers");
-constexpr int TC_BAR_SOFT = 1, TC_BAR_LOAD = 2;   // named barriers
+constexpr int TC_BAR_LOAD = 1;   // named barrier
 
 // 128-byte-swizzled operand blocks of 64 columns (128-byte rows, 8-row groups
 // 1024 bytes apart); lead: bytes between blocks of 64 columns, read for the
@@ -114,6 +120,26 @@ __device__ __forceinline__ void at_commit(uint64_t *bar)
 __device__ __forceinline__ void at_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void at_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // 32 lanes x 32 consecutive columns of tensor memory, without the wait
 __device__ __forceinline__ void at_ld32(uint32_t taddr, uint32_t *r)
 {
@@ -160,6 +186,35 @@ __device__ __forceinline__ void at_wait_ld(uint32_t *r)
                  : "memory");
 }
 __device__ __forceinline__ void at_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// nothing that uses these registers can be moved before this point
+__device__ __forceinline__ void at_pin(uint32_t *r)
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+// 16 columns times f
+__device__ __forceinline__ void at_scale16(uint32_t taddr, float f)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+    at_st16(taddr, r);
+}
 
 // bounded wait that gives up at once after another thread of the CTA did
 __device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort_word)
@@ -221,6 +276,43 @@ __device__ __forceinline__ void at_limits(const AttnArgs &a, const AttnSeq &s, i
     attn_keys(a, s, (row0 + rows - 1) / a.group, lo_max, d);
 }
 
+// Adds the infinite and NaN values that clean_v took out of the tiles at the
+// limits to the rows of O that see them: a warp's 32 rows in tensor memory.
+template <class T, class Walk, int KT>
+__device__ __noinline__ void at_restore(const AttnArgs &a, const Walk &w, int row0, int rows, int r, uint32_t taddr)
+{
+    int lo = 0, hi = 0, lo_max, hi_min;
+    if (r < rows)
+        attn_keys(a, w.s, (row0 + r) / a.group, lo, hi);
+    at_limits(a, w.s, row0, rows, lo_max, hi_min);
+    lo = max(lo, (w.t0 + w.ta()) * KT);
+    hi = min(hi, (w.t0 + w.tb()) * KT);
+    for (int c = 0; c < a.dim; c += 32) {
+        uint32_t u[32];
+        at_ld32(taddr + c, u);
+        at_wait_ld(u);
+        for (int j = lo; j < hi; ++j) {
+            if (j >= lo_max && j < hi_min) {
+                j = hi_min - 1;
+                continue;
+            }
+            const long long e = attn_slot(a, w.sp.b, w.h, j);
+            if (e < 0)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < a.dim) {
+                    const float x = Num16<T>::up(a.v[e + c + i]);
+                    if (!isfinite(x))
+                        u[i] = __float_as_uint(__uint_as_float(u[i]) + x);
+                }
+        }
+        __syncwarp();
+        at_st32(taddr + c, u);
+    }
+    at_wait_st();
+}
+
 template <class T, int DP, int NROW>
 __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(const AttnArgs a, const __grid_constant__ AttnMaps maps)
 {
@@ -231,7 +323,8 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::bar_off);
     uint32_t *tmem_word = reinterpret_cast<uint32_t *>(smem + C::misc_off);
     volatile int *abort_word = reinterpret_cast<volatile int *>(smem + C::misc_off + 4);
-    volatile int *poison = reinterpret_cast<volatile int *>(smem + C::misc_off + 16);   // [4], by unit
+    volatile int *poison = reinterpret_cast<volatile int *>(smem + C::misc_off + 16);   // V of this unit was cleaned
+    float2 *ml = reinterpret_cast<float2 *>(smem + C::ml_off);
     volatile int *armed_v = reinterpret_cast<volatile int *>(smem + C::misc_off + 32);  // [2], tile in the V stage
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int W_MMA = C::SOFT / 32;
@@ -239,7 +332,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     if (tid == 0) {
         tc_shared<M, DP>(a)[blockIdx.x].c1 = 0;
         const int full = a.tma ? 1 : C::LOAD;
-        mbar_init(&bar[TB_QF], C::LOAD);
+        mbar_init(&bar[TB_QF], a.tma_q ? 1 : C::LOAD);
         mbar_init(&bar[TB_QE], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[TB_KF + i], full);
@@ -249,6 +342,8 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             mbar_init(&bar[TB_VE + i], 1);
             mbar_init(&bar[TB_SF + i], 1);
             mbar_init(&bar[TB_PF + i], 128);
+            mbar_init(&bar[TB_P2 + i], 128);
+            mbar_init(&bar[TB_LF + i], 128);
             mbar_init(&bar[TB_OF + i], 1);
             mbar_init(&bar[TB_OE + i], 128);
         }
@@ -265,15 +360,28 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_trigger();   // the joining kernel may be launched; it waits for this one's end
-    const AttnSpan span = attn_span<M, KT>(a);
+    const AttnSpan span = attn_span<M, KT, TC_EX>(a);
     at_fence_before();
     __syncthreads();
     at_fence_after();
     const uint32_t tmem = *tmem_word;
-    AttnWalk<M, KT> w;
-    w.start(a, span);
+    // Each warp's place in the CTA's interval lies in shared memory: in registers
+    // it would push a row's scores out of them.
+    using Walk = AttnWalk<M, KT, TC_EX>;
+    static_assert(sizeof(Walk) <= 128, "walk");
+    Walk &w = *reinterpret_cast<Walk *>(smem + C::walk_off + warp * 128);
+    if (lane == 0)
+        w.start(a, span);
+    __syncwarp();
+    auto advance = [&]() {
+        __syncwarp();
+        if (lane == 0)
+            w.next(a);
+        __syncwarp();
+    };
 
     if (warp >= W_MMA) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_REST));
         if (warp == W_MMA) {
             // ================================================= MMA issuer
             // The whole warp walks and waits; one elected thread issues.
@@ -283,7 +391,9 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             const uint64_t qd = at_desc(smem_u32(smem + C::q_off), 16), kd = at_desc(smem_u32(smem + C::k_off), 16),
                            vd = at_desc(smem_u32(smem + C::v_off), KT * 128);
             uint32_t kc = 0, vc = 0, un = 0;          // tiles and units so far
-            uint32_t pc[2] = {0, 0}, oc[2] = {0, 0}, xc[2] = {0, 0};
+            // parities of the barrier pairs, a bit each (arrays would lie in local
+            // memory); given: bit r once row tile r's O has been handed over
+            uint32_t pc = 0, oc = 0, xc = 0, given = 0;
             bool ok = true, issued = false;
             auto wait = [&](int b, uint32_t parity) {
                 ok = ok && __all_sync(0xffffffffu, at_wait(&bar[b], parity & 1, a.status, abort_word));
@@ -320,17 +430,19 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 commit(TB_SF + buf);
                 issued = true;
             };
-            auto values = [&](int buf, int rt, uint32_t vs, bool acc) {
-                const uint64_t v = vd + vs * (C::tile / 16);
-                const uint32_t d = tmem + C::o_col + rt * DP, p = tmem + C::s_col + buf * 128;
+            // one half of a tile's keys: the first can start while the softmax
+            // still works on the second
+            auto values = [&](int buf, int rt, uint32_t vs, int half, bool acc) {
+                const uint64_t v = vd + vs * (C::tile / 16) + half * (KT / 32) * 128;
+                const uint32_t d = tmem + C::o_col + rt * DP, p = tmem + C::s_col + buf * 128 + half * (KT / 32) * 8;
                 if (at_elect()) {
 #pragma unroll
-                    for (int i = 0; i < KT / 16; ++i)
+                    for (int i = 0; i < KT / 32; ++i)
                         at_mma_ts(d, p + i * 8, v + i * 128, idesc_o, i > 0 || acc);
                 }
                 __syncwarp();
             };
-            for (; !w.done() && ok; w.next(a), ++un) {
+            for (; !w.done() && ok; advance(), ++un) {
                 const int nt = w.tb() - w.ta();
                 const int rows = min(M, w.s.n * a.group - w.rt * M);
                 const int nr = NROW == 2 && rows > 128 ? 2 : 1;   // row tiles with rows
@@ -359,9 +471,9 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     }
                     const int j0 = (w.t0 + w.ta() + j) * KT;
                     if (a.tma && (j0 < lo_max || j0 + KT > hi_min)) {
-                        if (!wait(TB_VX + vc % 2, xc[vc % 2]))
+                        if (!wait(TB_VX + vc % 2, xc >> (vc % 2)))
                             break;
-                        ++xc[vc % 2];
+                        xc ^= 1u << (vc % 2);
                     } else if (!wait(TB_VF + vc % 2, vc / 2)) {
                         break;
                     }
@@ -369,20 +481,25 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         break;
                     for (int r = 0; r < nr; ++r) {
                         const int buf = NROW == 2 ? r : j & 1;
-                        if (!wait(TB_PF + buf, pc[buf]))
+                        if (!wait(TB_PF + buf, pc >> buf))
                             break;
-                        ++pc[buf];
-                        if (j == 0 && oc[r] > 0 && !wait(TB_OE + r, oc[r] - 1))
+                        if (j == 0 && ((given >> r) & 1) && !wait(TB_OE + r, (oc >> r) ^ 1))
                             break;   // the last unit's O has been read
                         at_fence_after();
-                        values(buf, r, vc % 2, j > 0);
+                        values(buf, r, vc % 2, 0, j > 0);
+                        if (!wait(TB_P2 + buf, pc >> buf))
+                            break;
+                        pc ^= 1u << buf;
+                        at_fence_after();
+                        values(buf, r, vc % 2, 1, true);
                         if (NROW == 1)
                             commit(TB_PV);
                         if (NROW == 2 && more)
                             scores(buf, r, kc % 2);
                         if (!more) {
                             commit(TB_OF + r);
-                            ++oc[r];
+                            oc ^= 1u << r;
+                            given |= 1u << r;
                         }
                     }
                     if (!ok)
@@ -432,7 +549,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             // product.  Values outside the unit become zeros; infinite and NaN
             // ones at the limits are taken out and added to the rows that see
             // them at the end of the unit.
-            auto clean_v = [&](int stage, int j0, int lo_max, int hi_min, int u, int t, int nt) {
+            auto clean_v = [&](int stage, int j0, int lo_max, int hi_min, int t, int nt) {
                 unsigned char *v = smem + C::v_off + stage * C::tile;
                 for (int e = t; e < KT * CPR; e += nt) {
                     const int r = e / CPR, c = e % CPR, j = j0 + r;
@@ -455,22 +572,123 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         }
                     if (bad) {
                         *q = x;
-                        poison[u & 3] = 1;
+                        *poison = 1;
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
+            // The output of a unit, by the loader warps (so that the softmax goes on
+            // to the next unit): O from tensor memory, 16 rows x 128 bytes at a
+            // time through shared memory, so that 8 lanes write a row's 128 bytes
+            // together.  oc: parities, a bit for each row tile.
+            uint32_t oc = 0;
+            auto output = [&]() {
+                const int ta = w.ta(), tb = w.tb(), row0 = w.rt * M;
+                const int rows = min(M, w.s.n * a.group - row0);
+                const bool whole = ta == 0 && tb == w.nt;
+                const int quad = warp & 3;
+                unsigned char *stg = smem + C::stg_off + quad * 2048;
+                float *part = attn_part<M, DP>(a, blockIdx.x, ta == 0);
+                if (warp == W_MMA + 4 && lane == 0 && ta == 0 && tb < w.nt) {   // begins here, goes on in later CTAs
+                    TcShared *d = tc_shared<M, DP>(a) + blockIdx.x;
+                    d->q0 = w.s.q0;
+                    d->row0 = row0;
+                    d->rows = rows;
+                    d->h = w.h;
+                    d->c1 = w.c1();
+                }
+                for (int rt = 0; rt < NROW && rt * 128 < rows; ++rt) {
+                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_LF + rt], (oc >> rt) & 1, a.status, abort_word) &&
+                                                     at_wait(&bar[TB_OF + rt], (oc >> rt) & 1, a.status, abort_word))) {
+                        dead = true;
+                        return;
+                    }
+                    oc ^= 1u << rt;
+                    at_fence_after();
+                    const int r0 = rt * 128 + quad * 32, rr = r0 + lane;
+                    const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::o_col + rt * DP;
+                    const float2 mlr = ml[rr];
+                    if (*poison != 0)
+                        at_restore<T, Walk, KT>(a, w, row0, rows, rr, to);
+                    const int tok = (row0 + rr) / a.group, hq = w.h * a.group + (row0 + rr) - tok * a.group;
+                    // where this lane's row goes, in bytes; others are told by shuffle
+                    const long long mine = whole ? ((w.s.q0 + tok) * a.o_token + hq * a.o_head) * 2
+                                                 : (long long)rr * DP * 4;
+                    char *const dst = whole ? reinterpret_cast<char *>(a.out) : reinterpret_cast<char *>(part);
+                    const float inv = mlr.y == 0.f ? 0.f : 1.f / mlr.y;
+                    const int unit = lane & 7, step = whole ? 64 : 32;   // columns of 128 bytes
+                    // x[i]: the 16 rows' units of 16 bytes this lane writes to shared memory
+                    auto store = [&](int part16, int c0) {
+                        __syncwarp();
+                        uint4 x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 4 + (lane >> 3);
+                            x[i] = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((unit ^ (r & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = part16 * 16 + i * 4 + (lane >> 3);
+                            const long long at = __shfl_sync(0xffffffffu, mine, r);
+                            if (r0 + r < rows && c0 + unit * (step / 8) < a.dim)
+                                *reinterpret_cast<uint4 *>(dst + at + c0 * (128 / step) + unit * 16) = x[i];
+                        }
+                        __syncwarp();
+                    };
+#pragma unroll 1
+                    for (int c0 = 0; c0 < a.dim; c0 += step) {
+                        uint32_t v[32];
+                        at_ld32(to + c0, v);
+                        at_wait_ld(v);
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                v[i] = Num16<T>::down2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+                            if (c0 + 32 < a.dim) {
+                                uint32_t u[32];
+                                at_ld32(to + c0 + 32, u);
+                                at_wait_ld(u);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    v[16 + i] = Num16<T>::down2(__uint_as_float(u[2 * i]) * inv,
+                                                                __uint_as_float(u[2 * i + 1]) * inv);
+                            }
+                        }
+#pragma unroll
+                        for (int part16 = 0; part16 < 2; ++part16) {
+                            if ((lane >> 4) == part16) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<uint4 *>(stg + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                            }
+                            store(part16, c0);
+                        }
+                    }
+                    at_fence_before();
+                    mbar_arrive(&bar[TB_OE + rt]);
+                    if (rr < rows) {
+                        if (!whole) {
+                            part[M * DP + rr] = mlr.x;
+                            part[M * DP + M + rr] = mlr.y;
+                        } else if (a.lse) {
+                            a.lse[(size_t)(w.s.q0 + tok) * a.heads + hq] =
+                                mlr.y == 0.f ? -INFINITY : (mlr.x + log2f(mlr.y)) * kLn2;
+                        }
+                    }
+                }
+            };
             if (warp < W_MMA + 4) {
                 // ---- TMA: one warp for K, one for V (so that K never waits for
-                // a slot of V), each lane a box of the tile's keys
+                // a slot of V), each lane a box of the tile's keys; one for Q
                 const int x = warp - W_MMA - 1;
                 const int nbox = KT / max(a.tma, 1), nblk = (a.dim + 63) / 64;
                 const uint32_t bytes = KT * 128 * nblk;
                 const void *map = x ? &maps.v : &maps.k;
                 uint32_t n = 0;   // tiles so far
-                if (lane == 0)
+                if (lane == 0 && a.tma && x < 2)
                     prefetch_tensormap(map);
-                for (; a.tma && x < 2 && !w.done() && !dead; w.next(a)) {
+                for (; a.tma && x < 2 && !w.done() && !dead; advance()) {
                     const int ta = w.ta(), tb = w.tb();
                     int j = (w.t0 + ta) * KT + lane * a.tma;
                     int ahead = lane < nbox ? attn_page(a, w.sp.b, j, w.lo, w.hi) : 0;
@@ -506,8 +724,33 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         __syncwarp();
                     }
                 }
+                if (x == 2 && a.tma_q) {
+                    // ---- the query rows: 128 rows are 128 / group tokens x the group's heads
+                    uint32_t un = 0;
+                    if (lane == 0)
+                        prefetch_tensormap(&maps.q);
+                    for (; !w.done() && !dead; advance(), ++un) {
+                        const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
+                        const int nr = NROW == 2 && rows > 128 ? 2 : 1;
+                        if (un > 0 && !__all_sync(0xffffffffu,
+                                                  at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))) {
+                            dead = true;
+                            break;
+                        }
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&bar[TB_QF], nr * nblk * 128 * 128);
+                        __syncwarp();
+                        const int k = lane % nblk, r = lane / nblk;
+                        if (r < nr)
+                            tma_load_3d(smem + C::q_off + k * M * 128 + r * 128 * 128, &maps.q, k * 64, w.h * a.group,
+                                        w.s.q0 + (row0 + r * 128) / a.group, &bar[TB_QF]);
+                        __syncwarp();
+                    }
+                    if (lane == 0 && un > 0)
+                        mbar_wait(&bar[TB_QF], (un - 1) & 1, a.status);
+                }
                 // no copy may still be landing when the CTA exits
-                if (lane == 0)
+                if (lane == 0 && x < 2)
                     for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i)
                         mbar_wait(&bar[(x ? TB_VF : TB_KF) + i % 2], (i / 2) & 1, a.status);
                 __syncwarp();
@@ -515,20 +758,24 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 // ---- beside it: the query rows, and V at the limits
                 const int t = tid - C::SOFT - 128;
                 uint32_t un = 0, n = 0;
-                for (; !w.done(); w.next(a), ++un) {
+                for (; !w.done(); advance(), ++un) {
                     const int ta = w.ta(), tb = w.tb();
                     const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
-                    if (un > 0 && !at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))
+                    // (with Q on TMA these warps must not wait for it: its next use may
+                    // be over before they come here)
+                    if (un > 0 && !a.tma_q && !at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))
                         dead = true;
                     if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
                         break;
                     if (t == 0)
-                        poison[un & 3] = 0;
-                    load_q(t, C::LOAD, row0, rows);
-                    cp_async_commit();
-                    cp_async_wait<0>();
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(&bar[TB_QF]);
+                        *poison = 0;
+                    if (!a.tma_q) {
+                        load_q(t, C::LOAD, row0, rows);
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_arrive(&bar[TB_QF]);
+                    }
                     named_bar_sync(TC_BAR_LOAD, C::LOAD);   // the cleared poison flag is seen
                     int lo_max, hi_min;
                     at_limits(a, w.s, row0, rows, lo_max, hi_min);
@@ -544,10 +791,13 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                             dead = true;
                             break;
                         }
-                        clean_v(s % 2, j0, lo_max, hi_min, un, t, C::LOAD);
+                        clean_v(s % 2, j0, lo_max, hi_min, t, C::LOAD);
                         mbar_arrive(&bar[TB_VX + s % 2]);
                     }
                     n += tb - ta;
+                    // (a warp that gives up leaves here or at the next barrier)
+                    if (!__any_sync(0xffffffffu, dead))
+                        output();
                 }
             } else {
                 // ---- cp.async
@@ -560,7 +810,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 int lo_max = 0, hi_min = 0;
                 auto finish = [&](int i) {
                     if (pend_j0[i] >= 0)
-                        clean_v(pend_bar[i] - TB_VF, pend_j0[i], lo_max, hi_min, un, lt, C::LOAD);
+                        clean_v(pend_bar[i] - TB_VF, pend_j0[i], lo_max, hi_min, lt, C::LOAD);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(&bar[pend_bar[i]]);
                 };
@@ -606,7 +856,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     }
                     return o;
                 };
-                for (; !w.done(); w.next(a), ++un) {
+                for (; !w.done(); advance(), ++un) {
                     const int ta = w.ta(), tb = w.tb();
                     const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
                     long long o0 = slot(ta, tb, lt);
@@ -615,7 +865,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     if (bar_any(TC_BAR_LOAD, C::LOAD, dead || *abort_word != 0))
                         break;
                     if (lt == 0)
-                        poison[un & 3] = 0;
+                        *poison = 0;
                     load_q(lt, C::LOAD, row0, rows);
                     push(TB_QF, -1);
                     for (int t = ta; t < tb; ++t, ++kc) {
@@ -662,83 +912,84 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     flush();   // this unit's V is looked over with its own rows' limits
                     if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
                         break;
+                    output();
                 }
             }
         }
     } else {
         // ====================================================== softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFT));
         const int rt = warp >> 2, quad = warp & 3;
         const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16);
         const int rr = rt * 128 + quad * 32 + lane;   // row of the unit
-        uint32_t sc[2] = {0, 0}, oc = 0, pv = 0, un = 0;
+        uint32_t sc = 0, oc = 0, pv = 0;   // sc: parities, a bit each
         bool dead = false;
         const float sc2 = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
-        const float capc = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : 0.f, cap = a.softcap * kLog2e;
-        for (; !w.done(); w.next(a), ++un) {
-            const int ta = w.ta(), tb = w.tb();
-            const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
-            const bool active = rt * 128 < rows;
-            const bool whole = ta == 0 && tb == w.nt;
-            int lo = 0, hi = 0;
-            const int tok = (row0 + rr) / a.group, hq = w.h * a.group + (row0 + rr) - tok * a.group;
-            if (rr < rows)
-                attn_keys(a, w.s, tok, lo, hi);
+        for (; !w.done(); advance()) {
+            const int nt = w.tb() - w.ta();
+            const int rows = min(M, w.s.n * a.group - w.rt * M);
             float m = -INFINITY, l = 0.f;
-            if (active) {
-                for (int t = ta; t < tb && !dead; ++t) {
-                    const int buf = NROW == 2 ? rt : (t - ta) & 1;
-                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_SF + buf], sc[buf] & 1, a.status, abort_word))) {
+            if (rt * 128 < rows) {
+                // the row's keys, from the first of this CTA's tiles (rows past the
+                // end: all, so that they ask for no mask)
+                int l0 = 0, h0 = 0x7FFFFFFF;
+                if (rr < rows) {
+                    attn_keys(a, w.s, (w.rt * M + rr) / a.group, l0, h0);
+                    l0 -= (w.t0 + w.ta()) * KT;
+                    h0 -= (w.t0 + w.ta()) * KT;
+                }
+                for (int t = 0; t < nt; ++t, l0 -= KT, h0 -= KT) {
+                    const int buf = NROW == 2 ? rt : t & 1;
+                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_SF + buf], (sc >> buf) & 1, a.status, abort_word))) {
                         dead = true;
                         break;
                     }
-                    ++sc[buf];
+                    sc ^= 1u << buf;
                     at_fence_after();
                     const uint32_t ts = tq + C::s_col + buf * 128;
-                    const int j0 = (w.t0 + t) * KT;
-                    const int l0 = lo - j0, h0 = hi - j0;
                     const bool cut = __any_sync(0xffffffffu, l0 > 0 || h0 < KT);
-                    // first pass: the maximum (32 columns at a time, the next ones
-                    // on their way: all 128 at once would not leave the registers
-                    // of 512 threads); caps and masks go back to tensor memory
-                    uint32_t s[2][32];
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    at_ld32(ts, s[0]);
-#pragma unroll
-                    for (int c = 0; c < KT / 32; ++c) {
-                        uint32_t *x = s[c & 1];
-                        at_wait_ld(x);
-                        if (c + 1 < KT / 32)
-                            at_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
-                        if (a.softcap > 0.f || cut) {
+                    if (a.softcap > 0.f || cut) {
+                        // caps and masks, in tensor memory (kept short: they would
+                        // be most of the code)
+                        const float capc = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < KT; c += 32) {
+                            uint32_t x[32];
+                            at_ld32(ts + c, x);
+                            at_wait_ld(x);
                             if (a.softcap > 0.f) {
 #pragma unroll
                                 for (int i = 0; i < 32; ++i)
-                                    x[i] = __float_as_uint(capped(__uint_as_float(x[i]), capc, cap));
+                                    x[i] = __float_as_uint(capped(__uint_as_float(x[i]), capc, a.softcap * kLog2e));
                             }
-                            if (cut) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (32 * c + i < l0 || 32 * c + i >= h0)
-                                        x[i] = 0xFF800000u;   // -inf
-                            }
-                            at_st32(ts + 32 * c, x);
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < l0 || c + i >= h0)
+                                    x[i] = 0xFF800000u;   // -inf
+                            at_st32(ts + c, x);
                         }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2)
-                            mx[(i >> 1) & 3] =
-                                fmaxf(fmaxf(mx[(i >> 1) & 3], __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                    }
-                    if (a.softcap > 0.f || cut)
                         at_wait_st();
-                    at_ld32(ts, s[0]);
+                    }
+                    uint32_t s[KT];
+#pragma unroll
+                    for (int c = 0; c < KT; c += 32)
+                        at_ld32(ts + c, s + c);
+                    at_wait_ld(s);
+#pragma unroll
+                    for (int c = 32; c < KT; c += 32)
+                        at_pin(s + c);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; c += 2)
+                        mx[(c >> 1) & 3] =
+                            fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc2;
-                    const bool grow = top > m + TC_LAZY || (m == -INFINITY && top > m);
-                    if (__any_sync(0xffffffffu, grow)) {
+                    if (__any_sync(0xffffffffu, top > m + TC_LAZY || (m == -INFINITY && top > m))) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
                         m = mn;
                         l *= f;
-                        if (t > ta) {
+                        if (t > 0) {
                             // O holds the products up to the last tile's
                             if (NROW == 1 &&
                                 !__all_sync(0xffffffffu, at_wait(&bar[TB_PV], (pv - 1) & 1, a.status, abort_word))) {
@@ -746,155 +997,52 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                                 break;
                             }
                             at_fence_after();
-                            const uint32_t to = tq + C::o_col + rt * DP;
-                            for (int c = 0; c < a.dim; c += 32) {
-                                uint32_t v[32];
-                                at_ld32(to + c, v);
-                                at_wait_ld(v);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                                at_st32(to + c, v);
-                            }
+#pragma unroll 1
+                            for (int c = 0; c < a.dim; c += 16)
+                                at_scale16(tq + C::o_col + rt * DP + c, f);
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    // second pass: the weights, over the scores already read
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 k2 = make_float2(sc2, sc2), b2 = make_float2(-base, -base);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < KT / 32; ++c) {
-                        uint32_t *x = s[c & 1];
-                        at_wait_ld(x);
-                        if (c + 1 < KT / 32)
-                            at_ld32(ts + 32 * (c + 1), s[(c + 1) & 1]);
+                    for (int c = 0; c < KT; c += 32) {
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float u = exp2_approx(fmaf(__uint_as_float(x[2 * i]), sc2, -base));
-                            const float v = exp2_approx(fmaf(__uint_as_float(x[2 * i + 1]), sc2, -base));
-                            sum[(2 * i) & 3] += u;
-                            sum[(2 * i + 1) & 3] += v;
+                            float2 x = ffma2(make_float2(__uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1])),
+                                             k2, b2);
+                            x.x = exp2_approx(x.x);
+                            x.y = exp2_approx(x.y);
+                            sum[i & 1] = fadd2(sum[i & 1], x);
                             // the weights enter the product in the cache's type (at
                             // most half a step each); their sum stays unrounded
-                            p[i] = Num16<T>::down2(u, v);
+                            p[i] = Num16<T>::down2(x.x, x.y);
                         }
-                        at_st16(ts + 16 * c, p);
+                        at_st16(ts + c / 2, p);
+                        if (c + 32 == KT / 2 || c + 32 == KT) {
+                            at_wait_st();
+                            at_fence_before();
+                            mbar_arrive(&bar[(c + 32 == KT ? TB_P2 : TB_PF) + buf]);
+                        }
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    at_wait_st();
-                    at_fence_before();
-                    mbar_arrive(&bar[TB_PF + buf]);
+                    const float2 s2 = fadd2(sum[0], sum[1]);
+                    l += s2.x + s2.y;
                     ++pv;
                 }
-                // ---- the row's output
-                if (!dead && !__all_sync(0xffffffffu, at_wait(&bar[TB_OF + rt], oc & 1, a.status, abort_word)))
+                // the row's maximum and sum for the output, once the last unit's have
+                // been read (before its O was given back)
+                if (!dead && oc > 0 &&
+                    !__all_sync(0xffffffffu, at_wait(&bar[TB_OE + rt], (oc - 1) & 1, a.status, abort_word)))
                     dead = true;
                 if (!dead) {
                     ++oc;
-                    at_fence_after();
-                    const uint32_t to = tq + C::o_col + rt * DP;
-                    float *part = attn_part<M, DP>(a, blockIdx.x, ta == 0);
-                    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                    const bool bad = poison[un & 3] != 0;
-                    int lo_max = 0, hi_min = 0;
-                    if (bad)
-                        at_limits(a, w.s, row0, rows, lo_max, hi_min);
-                    // 16 rows x 128 bytes at a time through shared memory, so that
-                    // 8 lanes write a row's 128 bytes together
-                    unsigned char *stg = smem + C::stg_off + warp * 2048;
-                    const int step = whole ? 64 : 32;   // columns of 128 bytes
-                    for (int c0 = 0; c0 < a.dim; c0 += step) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int c = c0 + 32 * half;
-                            if (half && (!whole || c >= a.dim))
-                                break;
-                            uint32_t u[32];
-                            at_ld32(to + c, u);
-                            at_wait_ld(u);
-                            if (bad && rr < rows) {   // the values taken out by the loaders, for the rows that see them
-                                const int j1 = min(hi, (w.t0 + tb) * KT);
-                                for (int j = max(lo, (w.t0 + ta) * KT); j < j1; ++j) {
-                                    if (j >= lo_max && j < hi_min) {
-                                        j = hi_min - 1;
-                                        continue;
-                                    }
-                                    const long long e = attn_slot(a, w.sp.b, w.h, j);
-                                    if (e < 0)
-                                        continue;
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        if (c + i < a.dim) {
-                                            const float x = Num16<T>::up(a.v[e + c + i]);
-                                            if (!isfinite(x))
-                                                u[i] = __float_as_uint(__uint_as_float(u[i]) + x);
-                                        }
-                                }
-                            }
-                            if (whole) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    v[16 * half + i] = Num16<T>::down2(__uint_as_float(u[2 * i]) * inv,
-                                                                       __uint_as_float(u[2 * i + 1]) * inv);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    v[i] = u[i];
-                            }
-                        }
-#pragma unroll
-                        for (int part16 = 0; part16 < 2; ++part16) {
-                            __syncwarp();
-                            if ((lane >> 4) == part16) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    *reinterpret_cast<uint4 *>(stg + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = i * 4 + (lane >> 3), row = rt * 128 + quad * 32 + part16 * 16 + r;
-                                const int u = lane & 7;
-                                const uint4 x = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((u ^ (r & 7)) << 4));
-                                if (row >= rows || c0 + u * (step / 8) >= a.dim)
-                                    continue;
-                                if (whole) {
-                                    const int tk = (row0 + row) / a.group;
-                                    const int hd = w.h * a.group + (row0 + row) - tk * a.group;
-                                    *reinterpret_cast<uint4 *>(a.out + (w.s.q0 + tk) * a.o_token + hd * a.o_head + c0 +
-                                                               u * 8) = x;
-                                } else {
-                                    *reinterpret_cast<uint4 *>(part + (size_t)row * DP + c0 + u * 4) = x;
-                                }
-                            }
-                        }
-                    }
-                    at_fence_before();
-                    mbar_arrive(&bar[TB_OE + rt]);
-                    if (rr < rows) {
-                        if (whole) {
-                            if (a.lse)
-                                a.lse[(size_t)(w.s.q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                        } else {
-                            part[M * DP + rr] = m;
-                            part[M * DP + M + rr] = l;
-                        }
-                    }
+                    ml[rr] = make_float2(m, l);
+                    mbar_arrive(&bar[TB_LF + rt]);
                 }
             }
-            // the softmax warpgroups leave together
-            if (bar_any(TC_BAR_SOFT, C::SOFT, dead))
+            if (dead)
                 break;
-            if (tid == 0 && ta == 0 && tb < w.nt) {   // begins here, goes on in later CTAs
-                TcShared *d = tc_shared<M, DP>(a) + blockIdx.x;
-                d->q0 = w.s.q0;
-                d->row0 = row0;
-                d->rows = rows;
-                d->h = w.h;
-                d->c1 = attn_cta(w.sp, w.u0 + w.nt - 1);
-            }
         }
     }
     __syncthreads();
@@ -924,11 +1072,19 @@ template <class T, int DP, int NROW>
 cudaError_t launch_tc(const AttnArgs &args, const LaunchCfg &c)
 {
     using C = TcCfg<DP, NROW>;
+    auto kern = attn_tc_kernel<T, DP, NROW>;
     AttnArgs a = args;
     AttnMaps maps = {};
     if (!attn_maps(a, Num16<T>::kExp == 0x7F807F80u, C::KT, &maps, &a.tma, &a.heads_inner))
         a.tma = 0;
-    auto kern = attn_tc_kernel<T, DP, NROW>;
+    a.tma_q = a.tma != 0 && attn_q_map(a, Num16<T>::kExp == 0x7F807F80u, &maps.q);
+    // the register split asks for no more than the block is launched with
+    static const int regs = [&]() {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kern) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs * C::THREADS < C::SOFT * C::R_SOFT + 256 * C::R_REST)
+        return cudaErrorInvalidConfiguration;
     cudaError_t e = set_smem(kern, C::total);
     if (e != cudaSuccess)
         return e;

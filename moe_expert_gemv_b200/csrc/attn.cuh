@@ -9,7 +9,8 @@
 // line, cut into equal intervals, one per CTA: a batch of ragged
 // lengths keeps every SM busy to the end, one long context spreads over the
 // whole GPU, and nothing about the lengths is needed on the host (a captured
-// graph replays with new ones).  A unit that crosses CTA borders is finished
+// graph replays with new ones).  Each unit is EX places longer on the line
+// than its tiles: what it costs to begin and end one, in tiles.  A unit that crosses CTA borders is finished
 // by its last CTA to arrive, which adds the fp32 partial results in tile
 // order; nobody waits, and results do not depend on the order of arrival.
 #pragma once
@@ -135,7 +136,7 @@ __device__ __forceinline__ int attn_blocks(const AttnArgs &a, const AttnSeq &s)
     return (int)(((long long)s.n * a.group + M - 1) / M);
 }
 
-template <int M, int KT>
+template <int M, int KT, int EX>
 __device__ __forceinline__ long long attn_seq_tiles(const AttnArgs &a, const AttnSeq &s)
 {
     long long w = 0;
@@ -143,7 +144,7 @@ __device__ __forceinline__ long long attn_seq_tiles(const AttnArgs &a, const Att
     for (int rt = 0; rt < nb; ++rt) {
         int t0, nt, lo, hi;
         attn_tiles<M, KT>(a, s, rt, t0, nt, lo, hi);
-        w += nt;
+        w += EX + nt;
     }
     return w * a.kv_heads;
 }
@@ -158,7 +159,7 @@ struct AttnSpan {
 
 // Every warp works it out by itself, a lane a sequence: no block barrier, and
 // the lengths are read once (from L1 by the later warps).
-template <int M, int KT>
+template <int M, int KT, int EX>
 __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
 {
     const int lane = threadIdx.x & 31;
@@ -167,7 +168,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
     for (int b = lane; b < a.batch; b += 32) {
         if (blockIdx.x == 0 && threadIdx.x < 32 && a.kv_len[b] > (long long)a.max_pages * a.page_size)
             flag_status(a.status, QMOE_DEV_BAD_PAGE);
-        mine = attn_seq_tiles<M, KT>(a, attn_seq(a, b));
+        mine = attn_seq_tiles<M, KT, EX>(a, attn_seq(a, b));
         sum += mine;
     }
 #pragma unroll
@@ -184,7 +185,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
         return sp;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         if (a.batch > 32)
-            mine = b0 + lane < a.batch ? attn_seq_tiles<M, KT>(a, attn_seq(a, b0 + lane)) : 0;
+            mine = b0 + lane < a.batch ? attn_seq_tiles<M, KT, EX>(a, attn_seq(a, b0 + lane)) : 0;
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -204,20 +205,20 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
     return sp;
 }
 
-// the CTA that works on tile x of the line
+// the CTA whose interval holds place x of the line
 __device__ __forceinline__ int attn_cta(const AttnSpan &sp, long long x)
 {
     return (int)(((x + 1) * sp.ctas - 1) / sp.total);
 }
 
 // A walk over the units of a CTA's interval.
-template <int M, int KT>
+template <int M, int KT, int EX>
 struct AttnWalk {
     AttnSpan sp;
     AttnSeq s;
     int rt, nb, h;           // row block (of nb), K/V head
     int t0, nt, lo, hi;      // tiles and keys of the row block
-    long long u0;            // line index of the unit's first tile
+    long long u0;            // the unit's first place on the line; its tiles begin EX places on
 
     __device__ __forceinline__ void start(const AttnArgs &a, const AttnSpan &span)
     {
@@ -229,22 +230,25 @@ struct AttnWalk {
         u0 = sp.first;
         for (rt = 0;; ++rt) {
             attn_tiles<M, KT>(a, s, rt, t0, nt, lo, hi);
-            if (sp.x < u0 + (long long)nt * a.kv_heads || rt + 1 >= nb)
+            if (sp.x < u0 + (long long)(EX + nt) * a.kv_heads || rt + 1 >= nb)
                 break;
-            u0 += (long long)nt * a.kv_heads;
+            u0 += (long long)(EX + nt) * a.kv_heads;
         }
-        h = (int)((sp.x - u0) / nt);
-        u0 += (long long)h * nt;
+        h = (int)((sp.x - u0) / (EX + nt));
+        u0 += (long long)h * (EX + nt);
     }
-    __device__ __forceinline__ bool done() const { return sp.x >= sp.end; }
-    // the unit's tiles that are this CTA's: [ta, tb) of 0..nt
-    __device__ __forceinline__ int ta() const { return (int)(sp.x - u0); }
-    __device__ __forceinline__ int tb() const { return (int)(min(sp.end, u0 + nt) - u0); }
+    __device__ __forceinline__ bool done() const { return sp.x >= sp.end || sp.end <= u0 + EX; }
+    // the unit's tiles that are this CTA's: [ta, tb) of 0..nt, at least one
+    __device__ __forceinline__ int ta() const { return (int)max(sp.x - u0 - EX, 0ll); }
+    __device__ __forceinline__ int tb() const { return (int)min(sp.end - u0 - EX, (long long)nt); }
+    // first and last CTA with tiles of the unit
+    __device__ __forceinline__ int c0() const { return attn_cta(sp, u0 + EX); }
+    __device__ __forceinline__ int c1() const { return attn_cta(sp, u0 + EX + nt - 1); }
     __device__ __forceinline__ void next(const AttnArgs &a)
     {
-        u0 += nt;
+        u0 += EX + nt;
         sp.x = u0;
-        if (done())
+        if (sp.x >= sp.end)
             return;
         if (++h < a.kv_heads)
             return;
@@ -300,13 +304,25 @@ __device__ __forceinline__ void cp_async_wait()
 // Tensor maps of the cache: boxes of 64 columns x a.tma slots of one page and
 // head, 128-byte swizzled.
 struct AttnMaps {
-    CUtensorMap k, v;
+    CUtensorMap k, v, q;
 };
 
 // False where the cache's shape has no such map: pages must divide into
 // boxes of a multiple of 8 slots (the swizzle's period) that divide a tile of
 // kt keys, and the strides must nest.
 bool attn_maps(const AttnArgs &a, bool bf16, int kt, AttnMaps *m, int *rows, int *heads_inner);
+// q in boxes of 64 columns x the group's heads x 128 / group tokens; false
+// where a group does not divide 128 rows.
+bool attn_q_map(const AttnArgs &a, bool bf16, CUtensorMap *m);
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *map, int c0, int c1, int c2, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *map, int c0, int c1, int c2, int c3,
                                             uint64_t *bar)

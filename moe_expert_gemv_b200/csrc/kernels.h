@@ -244,6 +244,7 @@ struct AttnArgs {
     float scale, softcap;
     int window, causal;
     int tma;                         // rows of a TMA box of the cache, 0: none can be used
+    int tma_q;                       // q has a tensor map too
     int heads_inner;                 // order of the map's middle dimensions: heads, then slots
     float *part;                     // partial results of units that several CTAs share
     int *ctr;                        // their arrival counters, zero between calls
