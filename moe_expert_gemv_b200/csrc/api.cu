@@ -1008,6 +1008,8 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     a.tokens = batch->tokens;
     a.heads = attn->heads;
     a.group = group;
+    a.by_group = FastDiv((uint32_t)group);
+    a.by_page = FastDiv((uint32_t)cache->page_size);
     a.scale = attn->scale;
     a.softcap = attn->softcap;
     a.window = attn->window;

@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
         int lo_max, hi_min;
         {
             int d;
-            attn_keys(a, w.s, row0 / a.group, d, hi_min);
-            attn_keys(a, w.s, (row0 + rows - 1) / a.group, lo_max, d);
+            attn_keys(a, w.s, a.by_group(row0), d, hi_min);
+            attn_keys(a, w.s, a.by_group(row0 + rows - 1), lo_max, d);
         }
         auto fill_off = [&](int t, int r) {
             const int j = (w.t0 + t) * AM_KT + r;
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
             const int r = i / CPR, c = i % CPR;
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < rows && c * 8 < a.dim) {
-                const int tok = (row0 + r) / a.group, hq = w.h * a.group + (row0 + r) % a.group;
+                const int tok = a.by_group(row0 + r), hq = w.h * a.group + (row0 + r) - tok * a.group;
                 v = *reinterpret_cast<const uint4 *>(a.q + (w.s.q0 + tok) * a.q_token + hq * a.q_head + c * 8);
             }
             *reinterpret_cast<uint4 *>(smem + sw<DP>(r, c)) = v;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
             const int r = wr * 16 + g + 8 * i;
             lo[i] = hi[i] = 0;
             if (r < rows)
-                attn_keys(a, w.s, (row0 + r) / a.group, lo[i], hi[i]);
+                attn_keys(a, w.s, a.by_group(row0 + r), lo[i], hi[i]);
         }
         __syncthreads();
         uint32_t qf[DP <= 128 ? DP / 16 : 1][4];
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(AM_THREADS) attn_rows_kernel(const AttnArgs a)
                 v.z = fmaf(f, x.z, v.z);
                 v.w = fmaf(f, x.w, v.w);
             }
-            const int tok = (row0 + r) / a.group, hq = w.h * a.group + (row0 + r) % a.group;
+            const int tok = a.by_group(row0 + r), hq = w.h * a.group + (row0 + r) - tok * a.group;
             if (flag[1]) {   // the values taken out above, for the rows that see them
                 int klo, khi;
                 attn_keys(a, w.s, tok, klo, khi);

@@ -272,8 +272,8 @@ __device__ __forceinline__ void at_limits(const AttnArgs &a, const AttnSeq &s, i
                                           int &hi_min)
 {
     int d;
-    attn_keys(a, s, row0 / a.group, d, hi_min);
-    attn_keys(a, s, (row0 + rows - 1) / a.group, lo_max, d);
+    attn_keys(a, s, a.by_group(row0), d, hi_min);
+    attn_keys(a, s, a.by_group(row0 + rows - 1), lo_max, d);
 }
 
 // Adds the infinite and NaN values that clean_v took out of the tiles at the
@@ -283,7 +283,7 @@ __device__ __noinline__ void at_restore(const AttnArgs &a, const Walk &w, int ro
 {
     int lo = 0, hi = 0, lo_max, hi_min;
     if (r < rows)
-        attn_keys(a, w.s, (row0 + r) / a.group, lo, hi);
+        attn_keys(a, w.s, a.by_group(row0 + r), lo, hi);
     at_limits(a, w.s, row0, rows, lo_max, hi_min);
     lo = max(lo, (w.t0 + w.ta()) * KT);
     hi = min(hi, (w.t0 + w.tb()) * KT);
@@ -527,16 +527,14 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             // a block's query rows, by threads t of NT: each stays in its column
             auto load_q = [&](int t, int nt, int row0, int rows) {
                 const int c = t % CPR;
-                const int tok0 = row0 / a.group, rem = row0 - tok0 * a.group;
-                const float inv = 1.f / a.group;
+                const int tok0 = a.by_group(row0), rem = row0 - tok0 * a.group;
                 const bool in = c * 8 < a.dim;
                 if (c >= cpr)
                     return;
                 const int rows_q = NROW == 2 && rows <= 128 ? 128 : M;
 #pragma unroll 4
                 for (int r = t / CPR; r < rows_q; r += nt / CPR) {
-                    // (rem + r) / group: exact, the quotient is half a step off a whole number
-                    const int dt = (int)((rem + r + 0.5f) * inv);
+                    const int dt = a.by_group(rem + r);
                     const int hq = w.h * a.group + rem + r - dt * a.group;
                     const bool live = in && r < rows;
                     const long long e = (w.s.q0 + tok0 + dt) * a.q_token + hq * a.q_head + c * 8;
@@ -551,30 +549,28 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             // them at the end of the unit.
             auto clean_v = [&](int stage, int j0, int lo_max, int hi_min, int t, int nt) {
                 unsigned char *v = smem + C::v_off + stage * C::tile;
-                for (int e = t; e < KT * CPR; e += nt) {
-                    const int r = e / CPR, c = e % CPR, j = j0 + r;
-                    if (c >= cpr || (j >= lo_max && j < hi_min))
-                        continue;
-                    uint4 *q = reinterpret_cast<uint4 *>(v + at_sw(KT, r, c));
-                    if (j < w.lo || j >= w.hi) {
-                        *q = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint4 x = *q;
-                    uint32_t *p = reinterpret_cast<uint32_t *>(&x);
-                    bool bad = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (nonfinite2<T>(p[i])) {
-                            const float2 f = Num16<T>::up2(p[i]);
-                            p[i] = Num16<T>::down2(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
-                            bad = true;
+                const int r1 = min(max(lo_max - j0, 0), KT), r2 = max(min(hi_min - j0, KT), r1);
+                const int c = t % CPR;
+                if (c < cpr)
+                    for (int i = t / CPR; i < KT - (r2 - r1); i += nt / CPR) {
+                        const int r = i < r1 ? i : i + (r2 - r1), j = j0 + r;
+                        uint4 *q = reinterpret_cast<uint4 *>(v + at_sw(KT, r, c));
+                        if (j < w.lo || j >= w.hi) {
+                            *q = make_uint4(0, 0, 0, 0);
+                            continue;
                         }
-                    if (bad) {
-                        *q = x;
-                        *poison = 1;
+                        uint4 x = *q;
+                        if (nonfinite2<T>(x.x) || nonfinite2<T>(x.y) || nonfinite2<T>(x.z) || nonfinite2<T>(x.w)) {
+                            uint32_t *p = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = Num16<T>::up2(p[k]);
+                                p[k] = Num16<T>::down2(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
+                            }
+                            *q = x;
+                            *poison = 1;
+                        }
                     }
-                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             };
             // The output of a unit, by the loader warps (so that the softmax goes on
@@ -610,7 +606,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     const float2 mlr = ml[rr];
                     if (*poison != 0)
                         at_restore<T, Walk, KT>(a, w, row0, rows, rr, to);
-                    const int tok = (row0 + rr) / a.group, hq = w.h * a.group + (row0 + rr) - tok * a.group;
+                    const int tok = a.by_group(row0 + rr), hq = w.h * a.group + (row0 + rr) - tok * a.group;
                     // where this lane's row goes, in bytes; others are told by shuffle
                     const long long mine = whole ? ((w.s.q0 + tok) * a.o_token + hq * a.o_head) * 2
                                                  : (long long)rr * DP * 4;
@@ -694,7 +690,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     int ahead = lane < nbox ? attn_page(a, w.sp.b, j, w.lo, w.hi) : 0;
                     for (int t = ta; t < tb; ++t, ++n, j += KT) {
                         int page = ahead;
-                        const int slot = (int)((unsigned)j % (unsigned)a.page_size);
+                        const int slot = j - a.by_page(j) * a.page_size;
                         if (t + 1 < tb && lane < nbox)   // on its way while this tile's copies go out
                             ahead = attn_page(a, w.sp.b, j + KT, w.lo, w.hi);
                         if (n >= 2 && !__all_sync(0xffffffffu, at_wait(&bar[(x ? TB_VE : TB_KE) + n % 2], (n / 2 - 1) & 1,
@@ -743,7 +739,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         const int k = lane % nblk, r = lane / nblk;
                         if (r < nr)
                             tma_load_3d(smem + C::q_off + k * M * 128 + r * 128 * 128, &maps.q, k * 64, w.h * a.group,
-                                        w.s.q0 + (row0 + r * 128) / a.group, &bar[TB_QF]);
+                                        w.s.q0 + a.by_group(row0 + r * 128), &bar[TB_QF]);
                         __syncwarp();
                     }
                     if (lane == 0 && un > 0)
@@ -934,7 +930,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 // end: all, so that they ask for no mask)
                 int l0 = 0, h0 = 0x7FFFFFFF;
                 if (rr < rows) {
-                    attn_keys(a, w.s, (w.rt * M + rr) / a.group, l0, h0);
+                    attn_keys(a, w.s, a.by_group(w.rt * M + rr), l0, h0);
                     l0 -= (w.t0 + w.ta()) * KT;
                     h0 -= (w.t0 + w.ta()) * KT;
                 }

@@ -119,8 +119,8 @@ __device__ __forceinline__ void attn_tiles(const AttnArgs &a, const AttnSeq &s, 
 {
     const int rows = s.n * a.group;
     int d;
-    attn_keys(a, s, rt * M / a.group, lo, d);
-    attn_keys(a, s, (min(rt * M + M, rows) - 1) / a.group, d, hi);
+    attn_keys(a, s, a.by_group(rt * M), lo, d);
+    attn_keys(a, s, a.by_group(min(rt * M + M, rows) - 1), d, hi);
     if (hi <= lo) {   // nothing visible
         t0 = lo = hi = 0;
         nt = 1;
@@ -157,6 +157,13 @@ struct AttnSpan {
     int ctas;   // CTAs with work: each has at least one tile
 };
 
+// total * c / n, in 32 bits where that holds it (a 64-bit division is a
+// hundred instructions); at most 3 x 160 CTAs.
+__device__ __forceinline__ long long attn_place(long long total, int c, int n)
+{
+    return total < (1ll << 23) ? (long long)((uint32_t)total * (uint32_t)c / (uint32_t)n) : total * c / n;
+}
+
 // Every warp works it out by itself, a lane a sequence: no block barrier, and
 // the lengths are read once (from L1 by the later warps).
 template <int M, int KT, int EX>
@@ -176,9 +183,9 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     sp.total = sum;
     sp.ctas = (int)min(sum, (long long)gridDim.x);
-    const long long c = min((int)blockIdx.x, sp.ctas);
-    sp.x = sp.ctas ? sum * c / sp.ctas : 0;
-    sp.end = c < sp.ctas ? sum * (c + 1) / sp.ctas : sp.x;
+    const int c = min((int)blockIdx.x, sp.ctas);
+    sp.x = sp.ctas ? attn_place(sum, c, sp.ctas) : 0;
+    sp.end = c < sp.ctas ? attn_place(sum, c + 1, sp.ctas) : sp.x;
     sp.first = 0;
     sp.b = 0;
     if (sp.x >= sp.end)
@@ -208,6 +215,8 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
 // the CTA whose interval holds place x of the line
 __device__ __forceinline__ int attn_cta(const AttnSpan &sp, long long x)
 {
+    if (sp.total < (1ll << 23))
+        return (int)(((uint32_t)(x + 1) * (uint32_t)sp.ctas - 1) / (uint32_t)sp.total);
     return (int)(((x + 1) * sp.ctas - 1) / sp.total);
 }
 
@@ -234,7 +243,8 @@ struct AttnWalk {
                 break;
             u0 += (long long)(EX + nt) * a.kv_heads;
         }
-        h = (int)((sp.x - u0) / (EX + nt));
+        const long long d = sp.x - u0;
+        h = d < (1ll << 31) ? (int)((uint32_t)d / (uint32_t)(EX + nt)) : (int)(d / (EX + nt));
         u0 += (long long)h * (EX + nt);
     }
     __device__ __forceinline__ bool done() const { return sp.x >= sp.end || sp.end <= u0 + EX; }
@@ -267,7 +277,7 @@ struct AttnWalk {
 // or -1 for a page id outside the cache (flagged by the caller).
 __device__ __forceinline__ long long attn_slot(const AttnArgs &a, int b, int h, int j)
 {
-    const int pg = (int)((unsigned)j / (unsigned)a.page_size);
+    const int pg = a.by_page(j);
     const int id = __ldg(a.table + (size_t)b * a.max_pages + pg);
     if ((unsigned)id >= (unsigned)a.num_pages)
         return -1;
@@ -341,7 +351,7 @@ __device__ __forceinline__ int attn_page(const AttnArgs &a, int b, int j, int lo
 {
     if (j >= hi || j + a.tma <= lo)
         return a.num_pages;
-    return __ldg(a.table + (size_t)b * a.max_pages + (int)((unsigned)j / (unsigned)a.page_size));
+    return __ldg(a.table + (size_t)b * a.max_pages + a.by_page(j));
 }
 
 // ----------------------------------------------------------------- joining --
@@ -440,7 +450,7 @@ __device__ __forceinline__ void attn_join_row(const AttnArgs &a, int c0, int c1,
         }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int tok = row / a.group, hq = h * a.group + row - tok * a.group;
+    const int tok = a.by_group(row), hq = h * a.group + row - tok * a.group;
     uint16_t *dst = a.out + (q0 + tok) * a.o_token + hq * a.o_head + lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += 2)

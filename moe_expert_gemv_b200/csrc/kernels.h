@@ -230,6 +230,29 @@ constexpr int kTcMinTokens = 16;
 bool prefill_shape_supported(int hidden, int inter);
 
 // --------------------------------------------- attention over a paged cache --
+// n / d for 0 <= n < 2^31 by one multiplication (d >= 1): the rounded-up
+// reciprocal 2^(31 + l) / d, l = ceil(log2 d), is off by less than 2^-l / d.
+struct FastDiv {
+    uint32_t d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div), mul(0), shift(0)
+    {
+        if (div > 1) {
+            uint32_t l = 0;
+            while ((1ull << l) < div)
+                ++l;
+            mul = (uint32_t)(((1ull << (31 + l)) + div - 1) / div);
+            shift = l - 1;
+        }
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return d == 1 ? n : (int)(__umulhi((uint32_t)n, mul) >> shift);
+    }
+#endif
+};
+
 struct AttnArgs {
     const uint16_t *q, *k, *v;       // 16-bit numbers (fp16 or bf16)
     uint16_t *out;                   // [tokens][heads][dim] by strides
@@ -241,6 +264,7 @@ struct AttnArgs {
     long long page_stride, token_stride, head_stride;    // of the cache
     int batch, tokens, heads, kv_heads, group, dim;
     int page_size, num_pages, max_pages;
+    FastDiv by_group, by_page;
     float scale, softcap;
     int window, causal;
     int tma;                         // rows of a TMA box of the cache, 0: none can be used
