@@ -1048,9 +1048,10 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     }
 }
 
-// Joins the parts of the units that several CTAs shared: CTA (x, y) takes 32
-// rows of the unit that begins in CTA x, a warp a row at a time.
-constexpr int TJ_ROWS = 32, TJ_THREADS = 256;
+// Joins the parts of the units that several CTAs shared: CTA (x, y) takes 8
+// rows of the unit that begins in CTA x, a warp a row (32 rows a CTA, four to a
+// warp in turn, took 12.5 us where this takes 5: a row is two rounds of loads).
+constexpr int TJ_ROWS = 8, TJ_THREADS = 256;
 
 template <class T, int DP, int M>
 __global__ void __launch_bounds__(TJ_THREADS) attn_join_kernel(const AttnArgs a)
