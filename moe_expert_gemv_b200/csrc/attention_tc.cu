@@ -216,19 +216,6 @@ __device__ __forceinline__ void at_scale16(uint32_t taddr, float f)
     at_st16(taddr, r);
 }
 
-// bounded wait that gives up at once after another thread of the CTA did
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort_word)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    if (*abort_word)
-        return false;
-    if (mbar_wait(bar, parity, status))
-        return true;
-    *abort_word = 1;
-    return false;
-}
-
 // bounded wait until a stage has been armed for tile `n`
 __device__ __forceinline__ bool at_armed(volatile int *arm, int n, int32_t *status, volatile int *abort_word)
 {
@@ -246,12 +233,6 @@ __device__ __forceinline__ bool at_armed(volatile int *arm, int n, int32_t *stat
         }
     }
     return true;
-}
-
-// byte offset of 16-byte unit c of row r in an operand tile of `rows` rows
-__device__ __forceinline__ uint32_t at_sw(int rows, int r, int c)
-{
-    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // A unit that begins in a CTA and goes on in later ones, up to c1 (0: none).
@@ -1062,7 +1043,7 @@ __global__ void __launch_bounds__(TJ_THREADS) attn_join_kernel(const AttnArgs a)
         return;
     const int r1 = min((int)blockIdx.y * TJ_ROWS + TJ_ROWS, d.rows);
     for (int r = blockIdx.y * TJ_ROWS + (threadIdx.x >> 5); r < r1; r += TJ_THREADS / 32)
-        attn_join_row<T, M, DP>(a, blockIdx.x, d.c1, r, d.q0, d.row0 + r, d.h);
+        attn_join_row<T, M, DP, 8>(a, blockIdx.x, d.c1, r, d.q0, d.row0 + r, d.h);
 }
 
 template <class T, int DP, int NROW>

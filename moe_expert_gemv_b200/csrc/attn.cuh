@@ -178,9 +178,14 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
         mine = attn_seq_tiles<M, KT, EX>(a, attn_seq(a, b));
         sum += mine;
     }
+    const bool small = !__any_sync(0xffffffffu, sum >= (1 << 25));
+    if (small) {
+        sum = __reduce_add_sync(0xffffffffu, (unsigned)sum);
+    } else {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        for (int o = 16; o; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
     sp.total = sum;
     sp.ctas = (int)min(sum, (long long)gridDim.x);
     const int c = min((int)blockIdx.x, sp.ctas);
@@ -188,17 +193,29 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs &a)
     sp.end = c < sp.ctas ? attn_place(sum, c + 1, sp.ctas) : sp.x;
     sp.first = 0;
     sp.b = 0;
-    if (sp.x >= sp.end)
+    if (sp.x >= sp.end || a.batch == 1)
         return sp;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         if (a.batch > 32)
             mine = b0 + lane < a.batch ? attn_seq_tiles<M, KT, EX>(a, attn_seq(a, b0 + lane)) : 0;
-        long long incl = mine;
+        long long incl;
+        if (small) {
+            int v = (int)mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += u;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o)
+                    v += u;
+            }
+            incl = v;
+        } else {
+            incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += u;
+            }
         }
         const unsigned holds = __ballot_sync(0xffffffffu, sp.first + incl > sp.x);
         if (holds) {
@@ -282,6 +299,26 @@ __device__ __forceinline__ long long attn_slot(const AttnArgs &a, int b, int h, 
     if ((unsigned)id >= (unsigned)a.num_pages)
         return -1;
     return id * a.page_stride + (long long)(j - pg * a.page_size) * a.token_stride + h * a.head_stride;
+}
+
+// bounded wait that gives up at once after another thread of the CTA did
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort_word)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    if (*abort_word)
+        return false;
+    if (mbar_wait(bar, parity, status))
+        return true;
+    *abort_word = 1;
+    return false;
+}
+
+// byte offset of 16-byte unit c of row r in a tile of `rows` rows, in 128-byte
+// swizzled blocks of 64 columns
+__device__ __forceinline__ uint32_t at_sw(int rows, int r, int c)
+{
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // one look at a barrier, without being parked
@@ -370,9 +407,9 @@ __device__ __forceinline__ float *attn_part(const AttnArgs &a, int cta, int slot
 template <int NT>
 __device__ __forceinline__ bool attn_arrive(const AttnArgs &a, int c0, int c1, int *sm)
 {
-    __threadfence();
     named_bar_sync(1, NT);
     if (threadIdx.x == 0) {
+        __threadfence();   // everybody's parts: written before the barrier
         const int got = atomicAdd(a.ctr + c0, 1);
         *sm = got == c1 - c0;
         if (got == c1 - c0)
@@ -387,7 +424,7 @@ __device__ __forceinline__ bool attn_arrive(const AttnArgs &a, int c0, int c1, i
 // reads the maximum and sum of one part each, the parts' weights go round by
 // shuffles, and DP / 32 columns a lane are added in the parts' order.  r: row
 // of the unit; row: of the sequence, whose first token is row q0.
-template <class T, int M, int DP>
+template <class T, int M, int DP, int B>
 __device__ __forceinline__ void attn_join_row(const AttnArgs &a, int c0, int c1, int r, int q0, int row, int h)
 {
     const int lane = threadIdx.x & 31, np = c1 - c0 + 1;
@@ -403,11 +440,11 @@ __device__ __forceinline__ void attn_join_row(const AttnArgs &a, int c0, int c1,
         const float lk = k < np ? __ldcg(p + M * DP + M + r) : 0.f;
         const int n = min(32, np - k0);
         float w = 0.f;
-        // 8 parts' columns are on their way at once, the first 8 beside the maxima
-        for (int x0 = 0; x0 < n; x0 += 8) {
-            float v[8][V];
+        // B parts' columns are on their way at once, the first B beside the maxima
+        for (int x0 = 0; x0 < n; x0 += B) {
+            float v[B][V];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < B; ++x) {
                 const int kk = k0 + x0 + x;
                 const float *q = attn_part<M, DP>(a, c0 + kk, kk == 0) + (size_t)r * DP + lane * V;
 #pragma unroll
@@ -439,7 +476,7 @@ __device__ __forceinline__ void attn_join_row(const AttnArgs &a, int c0, int c1,
                     o[i] *= f;
             }
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
+            for (int x = 0; x < B; ++x) {
                 const float wx = __shfl_sync(0xffffffffu, w, x0 + x);
                 if (x0 + x < n) {
 #pragma unroll
