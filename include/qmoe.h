@@ -639,6 +639,9 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
  * and raise QMOE_DEV_BAD_TOKEN.  mask: uint32 [rows] of mask_stride words, or
  * mask_stride 0: one mask for all rows.  logits, out: [rows][vocab] by row
  * strides (elements); out may be logits.  rows 0..65535, vocab >= 1.
+ * workspace: logits_process_workspace_bytes(rows, max_history) bytes of device
+ * memory, 16-byte aligned, no initial contents required, not used by two calls
+ * that can run at the same time; 0 (and NULL allowed) for short histories.
  * ------------------------------------------------------------------------- */
 typedef struct qmoe_logit_rules {
     const int32_t *history;
@@ -656,9 +659,11 @@ typedef struct qmoe_logit_rules {
     int32_t max_bias;
 } qmoe_logit_rules;
 
+size_t logits_process_workspace_bytes(int32_t rows, int32_t max_history);
 qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, int64_t in_stride,
                            int32_t dtype, int32_t rows, int32_t vocab, void *out,
-                           int64_t out_stride, int32_t *status_dev, void *stream);
+                           int64_t out_stride, void *workspace, size_t workspace_bytes,
+                           int32_t *status_dev, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Format helpers (the packing reading of the "성능과 제약" section).

@@ -1020,9 +1020,17 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     return cuda_status(launch_attn(a, cache->dtype == QMOE_BF16, max_rows, launch_cfg(d, stream)));
 }
 
+size_t logits_process_workspace_bytes(int32_t rows, int32_t max_history)
+{
+    if (rows < 1 || rows > 65535 || max_history < 0 || max_history >= (1 << 20))
+        return 0;
+    return logits_workspace_bytes(rows, max_history);
+}
+
 qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, int64_t in_stride,
                            int32_t dtype, int32_t rows, int32_t vocab, void *out,
-                           int64_t out_stride, int32_t *status_dev, void *stream)
+                           int64_t out_stride, void *workspace, size_t workspace_bytes,
+                           int32_t *status_dev, void *stream)
 {
     if (!rules || !logits || !out || rows < 0 || vocab < 1 || in_stride < 0 || out_stride < 0 ||
         dtype < QMOE_F16 || dtype > QMOE_F32)
@@ -1040,7 +1048,7 @@ qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, in
                      (rules->mask && rules->mask_stride && rules->mask_stride < (vocab + 31) / 32) ||
                      (rules->history && rules->history_stride < rules->max_history)))
         return QMOE_ERR_INVALID_ARG;
-    if (rows > 65535 || rules->max_history >= (1 << 20) || rules->max_bias > kMaxLogitBias || vocab > (1 << 28))
+    if (rows > 65535 || rules->max_history >= (1 << 20) || rules->max_bias > kMaxLogitBias || vocab > (1 << 26))
         return QMOE_ERR_UNSUPPORTED;
     const size_t es = dtype == QMOE_F32 ? 4 : 2;
     const void *words[] = {rules->history, rules->history_len, rules->prompt_len, rules->repetition,
@@ -1048,8 +1056,11 @@ qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, in
     for (const void *p : words)
         if (!aligned(p, 4))
             return QMOE_ERR_ALIGNMENT;
-    if (!aligned(logits, es) || !aligned(out, es))
+    if (!aligned(logits, es) || !aligned(out, es) || (workspace && !aligned(workspace, 16)))
         return QMOE_ERR_ALIGNMENT;
+    const size_t need = rows > 0 ? logits_workspace_bytes(rows, rules->max_history) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return QMOE_ERR_WORKSPACE;
     qmoe_status s;
     DevState *d;
     if ((s = device_state(&d)) != QMOE_OK)
@@ -1077,7 +1088,7 @@ qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, in
     a.mask = rules->mask;
     a.mask_stride = rules->mask_stride;
     a.status = status_dev ? status_dev : d->status;
-    return cuda_status(launch_logits(a, dtype, launch_cfg(d, stream)));
+    return cuda_status(launch_logits(a, dtype, workspace, launch_cfg(d, stream)));
 }
 
 qmoe_status qmoe_pack_codes(const uint8_t *codes, int32_t rows, int32_t cols, int32_t bits,

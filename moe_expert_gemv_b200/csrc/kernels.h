@@ -314,10 +314,13 @@ struct LogitsArgs {
     int max_bias;
     const uint32_t *mask;            // [rows] of mask_stride words, or null
     long long mask_stride;
+    int *begin, *sorted;             // workspace: the histories sorted by slices
     int32_t *status;
 };
 constexpr int kMaxLogitBias = 1024;
-cudaError_t launch_logits(const LogitsArgs &a, int dtype, const LaunchCfg &c);
+constexpr int kLogitsUnsorted = 2048;   // histories up to this long need no workspace
+size_t logits_workspace_bytes(int rows, int max_history);
+cudaError_t launch_logits(const LogitsArgs &a, int dtype, void *ws, const LaunchCfg &c);
 
 // ------------------------------------------------------------ pack helpers --
 cudaError_t launch_pack(const uint8_t *codes, int rows, int cols, int bits, uint32_t *packed,

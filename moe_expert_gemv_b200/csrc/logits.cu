@@ -9,144 +9,459 @@
 //   mask bit v clear: x = -inf
 //
 // Memory bound: the row is read once and written once (in place if asked),
-// everything else is small.  Each CTA owns a slice of the vocabulary and
-// keeps one 32-bit word per token of it in shared memory: the count n, a
-// "seen" bit and the number of the token's first bias entry; counting is
-// integer, so the order of the atomics does not show.
+// everything else is small.  A CTA takes a slice of a row: its logits are on
+// their way to registers, 16 bytes a load, while the slice's part of the
+// history is counted into one 32-bit word per token in shared memory (the
+// count n, a "seen" bit and the number of the token's first bias entry).  The
+// slice is written, masked, and then its tokens that have a word once more:
+// whoever takes the word out (an exchange with zero) writes the token -- few
+// threads with a token each, where a look at every word by the thread that
+// holds the logit sends whole warps through the rules for one lane (109 us
+// instead of 93 for this kernel alone on the case below).  A token that no rule touches leaves
+// as the bits it came.  Counting is integer, so the order of the atomics does
+// not show.
+// A short history is looked through by every slice.  A long one is first
+// sorted by ranges of slices, in a kernel of a CTA per row that the slices'
+// kernel overlaps (its logits do not wait for it).  Measured, 256 x 262144
+// bf16 with histories of up to 12000 tokens, a mask (44 us without a history,
+// which is 6.4 TB/s): 92 us.  There the looking through unsorted histories
+// took 112 us, a full sort by slice 106 us; tokens counted in hash tables and
+// written by a second kernel 87 us, but 7.6 us instead of 4.2 for one short
+// row; a cluster's CTAs counting into one another's words 238 us (texts repeat
+// a few tokens, whose words all lie in one CTA); slices taken through shared
+// memory by bulk copies 128 us.  48 x 151937 fp32 with everything on: 21 us.
+#include <algorithm>
+
 #include "attn.cuh"
 
 namespace qmoe {
 namespace {
 
-constexpr int LG_THREADS = 512;
-constexpr int LG_TILE = 8192;                 // vocabulary entries per CTA
 constexpr uint32_t LG_SEEN = 1u << 31;
 constexpr int LG_BIAS_SHIFT = 20;             // 11 bits: 1 + index of the first entry with this id
 constexpr uint32_t LG_COUNT = (1u << LG_BIAS_SHIFT) - 1;
+constexpr int LG_THREADS = 256;
+constexpr int LG_RANGES = 8;                  // ranges of slices that a history is sorted by
+constexpr int LG_SORT = 1024;                 // threads of the sort
 
 template <class T>
 struct Elem;
 template <>
 struct Elem<float> {
     using raw = float;
+    static constexpr uint32_t none = 0xFF800000u;   // -inf, in every element of a word
     static __device__ __forceinline__ float up(float v) { return v; }
     static __device__ __forceinline__ float down(float v) { return v; }
 };
 template <>
 struct Elem<__half> : Num16<__half> {
     using raw = uint16_t;
+    static constexpr uint32_t none = 0xFC00FC00u;
 };
 template <>
 struct Elem<__nv_bfloat16> : Num16<__nv_bfloat16> {
     using raw = uint16_t;
+    static constexpr uint32_t none = 0xFF80FF80u;
 };
 
-struct RowRule {
-    float rep, pres, freq;
-};
-
-__device__ __forceinline__ float apply(float x, uint32_t w, const RowRule &r, const float *bsum)
+// places that a row begins behind a 16-byte boundary
+template <class R>
+__device__ __forceinline__ int row_shift(const LogitsArgs &a, int row)
 {
-    if (w & LG_SEEN)
-        x = x > 0.f ? x / r.rep : x * r.rep;
-    const uint32_t n = w & LG_COUNT;
-    if (n)
-        x = x - r.freq * (float)n - r.pres;
-    const uint32_t b = (w & ~LG_SEEN) >> LG_BIAS_SHIFT;
-    if (b)
-        x += bsum[b - 1];
-    return x;
+    return (int)((reinterpret_cast<uintptr_t>(static_cast<const R *>(a.in) + row * a.in_stride) % 16) / sizeof(R));
 }
 
-template <class T>
-__global__ void __launch_bounds__(LG_THREADS) logits_kernel(const LogitsArgs a)
+// -------------------------------------------------------------------- sort --
+// CTA per row: a.sorted[row][..] the row's valid tokens by range of `per`
+// slices (the sign bit: behind the prompt), a.begin[row][r] where range r's
+// begin.  So each slice looks through its own range's tokens; 8 ranges leave
+// at most an eighth more of them than a sort by slice, which costs more than
+// that (31 us instead of 18, 256 rows of up to 12000 tokens).  Counting
+// sort: the lanes of a warp whose tokens fall into one range take their places
+// together, from a counter of the warp's own.
+template <class T, int TILE>
+__global__ void __launch_bounds__(LG_SORT) logits_sort_kernel(const LogitsArgs a, int per)
 {
-    extern __shared__ uint32_t lsm[];
-    uint32_t *word = lsm;                                        // [LG_TILE]
-    int *bid = reinterpret_cast<int *>(lsm + LG_TILE);           // [max_bias]
+    using R = typename Elem<T>::raw;
+    constexpr int NW = LG_SORT / 32, NC = LG_RANGES * NW, KEEP = 12;
+    __shared__ int cnt[NC];   // [range][warp]
+    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    const int n = min(max(a.history_len[row], 0), a.max_history);
+    const int p = a.prompt_len ? a.prompt_len[row] : 0;
+    const int32_t *h = a.history + row * a.history_stride;
+    int *out = a.sorted + (size_t)row * a.max_history;
+    const int shift = row_shift<R>(a, row);
+    const float inv = 1.f / (float)(TILE * per);
+    if (tid < NC)
+        cnt[tid] = 0;
+    __syncthreads();
+    // place of this lane's token within its (range, warp); -1: not a token
+    auto take = [&](int id, int &r) {
+        const bool ok = (unsigned)id < (unsigned)a.vocab;
+        // a range more or less by rounding at a border would be wrong: settled in integers
+        r = ok ? (int)((float)(id + shift) * inv) : LG_RANGES;
+        if (ok) {
+            r -= r * (TILE * per) > id + shift;
+            r += (r + 1) * (TILE * per) <= id + shift;
+        }
+        unsigned peers = 0xffffffffu;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {   // r <= 8
+            const unsigned ones = __ballot_sync(0xffffffffu, (r >> b) & 1);
+            peers &= (r >> b) & 1 ? ones : ~ones;
+        }
+        const int lead = __ffs(peers) - 1;
+        int at = 0;
+        if (lane == lead && ok) {
+            at = cnt[r * NW + warp];
+            cnt[r * NW + warp] = at + __popc(peers);
+        }
+        __syncwarp();
+        at = __shfl_sync(0xffffffffu, at, lead) + __popc(peers & ((1u << lane) - 1));
+        if (!ok && id != -1)
+            flag_status(a.status, QMOE_DEV_BAD_TOKEN);
+        return ok ? at : -1;
+    };
+    int id[KEEP], at[KEEP], r[KEEP];   // the first tokens' stay in registers
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        id[k] = k * LG_SORT + tid < n ? __ldg(h + k * LG_SORT + tid) : -1;
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k) {
+        at[k] = -1;
+        if (k * LG_SORT < n)
+            at[k] = take(id[k], r[k]);
+    }
+    for (int i = KEEP * LG_SORT; i < n; i += LG_SORT) {
+        int x;
+        take(i + tid < n ? __ldg(h + i + tid) : -1, x);
+    }
+    __syncthreads();
+    if (warp == 0) {   // counts to places
+        int sum = 0;
+#pragma unroll
+        for (int k = 0; k < LG_RANGES; ++k) {
+            const int c = cnt[k * NW + lane];
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += u;
+            }
+            cnt[k * NW + lane] = sum + incl - c;
+            if (lane == 0)
+                a.begin[(size_t)row * (LG_RANGES + 1) + k] = sum;
+            sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0)
+            a.begin[(size_t)row * (LG_RANGES + 1) + LG_RANGES] = sum;
+    }
+    __syncthreads();
+    auto put = [&](int i, int id, int r, int at) {
+        out[cnt[r * NW + warp] + at] = i >= p ? id | (int)0x80000000 : id;
+    };
+    int first[LG_RANGES];   // the warp's places that the kept tokens have taken
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        if (at[k] >= 0)
+            put(k * LG_SORT + tid, id[k], r[k], at[k]);
+    if (n > KEEP * LG_SORT) {
+        // the rest once more: their places follow on the kept ones'
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < LG_RANGES; ++k) {
+            int c = 0;
+#pragma unroll
+            for (int j = 0; j < KEEP; ++j)
+                c += __popc(__ballot_sync(0xffffffffu, at[j] >= 0 && r[j] == k));
+            first[k] = c;
+        }
+        __syncwarp();
+        if (lane == 0)
+#pragma unroll
+            for (int k = 0; k < LG_RANGES; ++k)
+                cnt[k * NW + warp] += first[k];
+        __syncwarp();
+        for (int i = KEEP * LG_SORT; i < n; i += LG_SORT) {
+            int x;
+            const int y = i + tid < n ? __ldg(h + i + tid) : -1;
+            const int z = take(y, x);   // counts on from the warp's places
+            if (z >= 0)
+                out[z] = i + tid >= p ? y | (int)0x80000000 : y;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ slices --
+// CTA (row, t): TILE places of the row; slices later than rows in the grid's
+// order, because a text's tokens crowd in the first slices and those should
+// not come last.  WORDS: there is a history or a bias;
+// SORTED: the history has been sorted.
+template <class T, int TILE, bool WORDS, bool SORTED, bool MASK>
+__global__ void __launch_bounds__(LG_THREADS, 5) logits_kernel(const LogitsArgs a, int per)
+{
+    using R = typename Elem<T>::raw;
+    constexpr int NT = LG_THREADS;
+    constexpr int E = 16 / (int)sizeof(R);   // elements of a 16-byte unit
+    constexpr int NV = TILE / (E * NT);
+    extern __shared__ __align__(16) uint32_t lsm[];
+    uint32_t *word = lsm;                                        // [TILE]
+    int *bid = reinterpret_cast<int *>(lsm + TILE);              // [max_bias]
     float *bval = reinterpret_cast<float *>(bid + a.max_bias);   // [max_bias]
     float *bsum = bval + a.max_bias;                             // [max_bias]
-    using R = typename Elem<T>::raw;
-    const int row = blockIdx.y, tid = threadIdx.x;
-    const int v0 = blockIdx.x * LG_TILE, nv = min(LG_TILE, a.vocab - v0);
-    for (int i = tid; i < nv; i += LG_THREADS)
-        word[i] = 0;
-    for (int i = tid; i < a.max_bias; i += LG_THREADS) {
-        bid[i] = a.bias_ids[(size_t)row * a.max_bias + i];
-        bval[i] = a.bias[(size_t)row * a.max_bias + i];
+    const int row = blockIdx.x, slice = blockIdx.y, tid = threadIdx.x;
+    const R *in = static_cast<const R *>(a.in) + row * a.in_stride;
+    R *out = static_cast<R *>(a.out) + row * a.out_stride;
+    const uint32_t *mask = MASK ? a.mask + row * a.mask_stride : nullptr;
+    const int shift = row_shift<R>(a, row), v0 = slice * TILE - shift;
+    if (v0 >= a.vocab)
+        return;
+    const bool vec_out = reinterpret_cast<uintptr_t>(out - shift) % 16 == 0;
+    union Vec {
+        uint4 q;
+        uint32_t w[4];
+        R e[E];
+    };
+    Vec x[NV];
+    uint32_t bits[NV];   // the mask word of each unit's first token
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = v0 + (k * NT + tid) * E;
+        if (v >= 0 && v + E <= a.vocab) {
+            x[k].q = *reinterpret_cast<const uint4 *>(in + v);
+            if (MASK)
+                bits[k] = __ldg(mask + (v >> 5));
+        } else if (v + E > 0 && v < a.vocab) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (v + i >= 0 && v + i < a.vocab)
+                    x[k].e[i] = in[v + i];
+        }
     }
-    __syncthreads();
-    if (a.history) {
-        const int n = min(max(a.history_len[row], 0), a.max_history);
-        const int p = a.prompt_len ? a.prompt_len[row] : 0;
-        const int32_t *h = a.history + row * a.history_stride;
-        for (int i = tid; i < n; i += LG_THREADS) {
-            const int id = h[i];
+    // the tokens to look through, [begin, end) of ids; a thread's first four
+    // stay in registers between the two times
+    constexpr int KEEP = 4;
+    const int32_t *ids = nullptr;
+    int begin = 0, end = 0, p = 0, kept[KEEP];
+    if (WORDS) {
+#pragma unroll
+        for (int k = 0; k < TILE / (4 * NT); ++k)
+            reinterpret_cast<uint4 *>(word)[k * NT + tid] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < a.max_bias; i += NT) {
+            bid[i] = a.bias_ids[(size_t)row * a.max_bias + i];
+            bval[i] = a.bias[(size_t)row * a.max_bias + i];
+        }
+        __syncthreads();
+        if (SORTED) {
+            pdl_wait();   // the history has been sorted
+            const int *b = a.begin + (size_t)row * (LG_RANGES + 1) + slice / per;
+            begin = __ldcg(b);
+            end = __ldcg(b + 1);
+            ids = a.sorted + (size_t)row * a.max_history;
+        } else if (a.history) {
+            end = min(max(a.history_len[row], 0), a.max_history);
+            p = a.prompt_len ? a.prompt_len[row] : 0;
+            ids = a.history + row * a.history_stride;
+        }
+        auto count = [&](int i, int id) {
+            const bool made = SORTED ? id < 0 : i >= p;
+            const int token = SORTED ? id & 0x7FFFFFFF : id;
+            const unsigned u = (unsigned)(token - v0);
+            if (!SORTED && (unsigned)id >= (unsigned)a.vocab) {
+                if (id != -1 && slice == 0)
+                    flag_status(a.status, QMOE_DEV_BAD_TOKEN);
+            } else if (u < (unsigned)TILE) {
+                if (made)
+                    atomicAdd(word + u, 1u);   // a count says "seen" too
+                else
+                    atomicOr(word + u, LG_SEEN);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            kept[k] = begin + k * NT + tid < end ? __ldcg(ids + begin + k * NT + tid) : -1;
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) {
+            const int i = begin + k * NT + tid;
+            if (i < end)
+                count(i, kept[k]);
+        }
+        for (int i0 = begin + KEEP * NT + tid; i0 < end; i0 += 8 * NT) {
+            int id[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                id[k] = i0 + k * NT < end ? __ldcg(ids + i0 + k * NT) : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + k * NT < end)
+                    count(i0 + k * NT, id[k]);
+        }
+        for (int i = tid; i < a.max_bias; i += NT) {
+            const int id = bid[i];
             const unsigned u = (unsigned)(id - v0);
-            if (u < (unsigned)nv) {
-                atomicOr(&word[u], LG_SEEN);
-                if (i >= p)
-                    atomicAdd(&word[u], 1u);
-            } else if (blockIdx.x == 0 && (unsigned)id >= (unsigned)a.vocab && id != -1) {
-                flag_status(a.status, QMOE_DEV_BAD_TOKEN);
-            }
-        }
-    }
-    for (int i = tid; i < a.max_bias; i += LG_THREADS) {
-        const int id = bid[i];
-        const unsigned u = (unsigned)(id - v0);
-        if (u < (unsigned)nv) {
-            float sum = 0.f;
-            bool first = true;
-            for (int k = 0; k < a.max_bias; ++k)
-                if (bid[k] == id) {
-                    if (k < i) {
-                        first = false;
-                        break;
-                    }
-                    sum += bval[k];
+            if ((unsigned)id >= (unsigned)a.vocab) {
+                if (id != -1 && slice == 0)
+                    flag_status(a.status, QMOE_DEV_BAD_TOKEN);
+            } else if (u < (unsigned)TILE) {
+                // an id's entries add up, in their order, at its first one
+                float sum = 0.f;
+                bool first = true;
+#pragma unroll 8
+                for (int k = 0; k < a.max_bias; ++k) {
+                    const bool same = bid[k] == id;
+                    first = first && !(same && k < i);
+                    if (same)
+                        sum += bval[k];
                 }
-            if (first) {
-                bsum[i] = sum;
-                atomicOr(&word[u], (uint32_t)(i + 1) << LG_BIAS_SHIFT);
+                if (first) {
+                    bsum[i] = sum;
+                    atomicOr(word + u, (uint32_t)(i + 1) << LG_BIAS_SHIFT);
+                }
             }
-        } else if (blockIdx.x == 0 && (unsigned)id >= (unsigned)a.vocab && id != -1) {
-            flag_status(a.status, QMOE_DEV_BAD_TOKEN);
         }
     }
-    __syncthreads();
-    RowRule r;
-    r.rep = a.repetition ? a.repetition[row] : 1.f;
-    r.pres = a.presence ? a.presence[row] : 0.f;
-    r.freq = a.frequency ? a.frequency[row] : 0.f;
-    const R *in = static_cast<const R *>(a.in) + row * a.in_stride + v0;
-    R *out = static_cast<R *>(a.out) + row * a.out_stride + v0;
-    const uint32_t *mask = a.mask ? a.mask + row * a.mask_stride : nullptr;
-    for (int i = tid; i < nv; i += LG_THREADS) {
-        float x = apply(Elem<T>::up(in[i]), word[i], r, bsum);
-        if (mask && !((mask[(v0 + i) >> 5] >> ((v0 + i) & 31)) & 1u))
-            x = -INFINITY;
-        out[i] = Elem<T>::down(x);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = v0 + (k * NT + tid) * E;
+        if (v >= 0 && v + E <= a.vocab) {
+            if (MASK) {
+                uint32_t m = bits[k] >> (v & 31);
+                if ((v & 31) > 32 - E)   // the unit goes on in the next word
+                    m |= __ldg(mask + (v >> 5) + 1) << (32 - (v & 31));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // an element's bit becomes a mask of its width
+                    const uint32_t keep = E == 4 ? 0u - ((m >> j) & 1u)
+                                                 : ((m >> (2 * j)) & 1u) * 0xFFFFu | ((m >> (2 * j + 1)) & 1u) * 0xFFFF0000u;
+                    x[k].w[j] = (x[k].w[j] & keep) | (Elem<T>::none & ~keep);
+                }
+            }
+            if (vec_out) {
+                __stcs(reinterpret_cast<uint4 *>(out + v), x[k].q);
+            } else {   // the output begins elsewhere within 16 bytes than the input
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    out[v + i] = x[k].e[i];
+            }
+        } else if (v + E > 0 && v < a.vocab) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (v + i >= 0 && v + i < a.vocab)
+                    out[v + i] = MASK && !((mask[(v + i) >> 5] >> ((v + i) & 31)) & 1u) ? Elem<T>::down(-INFINITY) : x[k].e[i];
+        }
     }
+    if (!WORDS)
+        return;
+    const float rep = a.repetition ? a.repetition[row] : 1.f;
+    const float pres = a.presence ? a.presence[row] : 0.f;
+    const float freq = a.frequency ? a.frequency[row] : 0.f;
+    __syncthreads();   // the counts are complete, the slice is written
+    // Whoever takes a token's word out writes the token, four at a time so that
+    // their logits come together (what the mask let through has its old value,
+    // in place too).
+    auto settle = [&](const int *id) {
+        uint32_t w[KEEP], m[KEEP];
+        R y[KEEP];
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) {
+            const unsigned u = (unsigned)(id[k] - v0);
+            w[k] = 0;
+            if ((unsigned)id[k] < (unsigned)a.vocab && u < (unsigned)TILE &&
+                *const_cast<volatile uint32_t *>(word + u) != 0)
+                w[k] = atomicExch(word + u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (w[k]) {
+                y[k] = in[id[k]];
+                m[k] = MASK ? __ldg(mask + (id[k] >> 5)) >> (id[k] & 31) : 1u;
+            }
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (w[k] && (m[k] & 1u)) {
+                float v = Elem<T>::up(y[k]);
+                const uint32_t c = w[k] & LG_COUNT, b = (w[k] & ~LG_SEEN) >> LG_BIAS_SHIFT;
+                if (c || (w[k] & LG_SEEN))
+                    v = v > 0.f ? v / rep : v * rep;
+                if (c)
+                    v = v - freq * (float)c - pres;
+                if (b)
+                    v += bsum[b - 1];
+                out[id[k]] = Elem<T>::down(v);
+            }
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        kept[k] = begin + k * NT + tid < end ? (SORTED ? kept[k] & 0x7FFFFFFF : kept[k]) : -1;
+    settle(kept);
+    for (int i0 = begin + KEEP * NT + tid; i0 < end; i0 += KEEP * NT) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) {
+            const int id = i0 + k * NT < end ? __ldcg(ids + i0 + k * NT) : -1;
+            kept[k] = SORTED && i0 + k * NT < end ? id & 0x7FFFFFFF : id;
+        }
+        settle(kept);
+    }
+    for (int i0 = tid; i0 < a.max_bias; i0 += KEEP * NT) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            kept[k] = i0 + k * NT < a.max_bias ? bid[i0 + k * NT] : -1;
+        settle(kept);
+    }
+}
+
+template <class T, int TILE>
+cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
+{
+    using R = typename Elem<T>::raw;
+    const int slices = (int)((a.vocab + 16 / (long long)sizeof(R) - 1 + TILE - 1) / TILE);
+    LaunchCfg c2 = c;
+    c2.pdl = false;
+    const dim3 grid(a.rows, slices);
+    if (a.max_history == 0 && a.max_bias == 0)
+        return a.mask ? launch_ex(logits_kernel<T, TILE, false, false, true>, grid, dim3(LG_THREADS), 0, c2, 1, a, 1)
+                      : launch_ex(logits_kernel<T, TILE, false, false, false>, grid, dim3(LG_THREADS), 0, c2, 1, a, 1);
+    const size_t smem = TILE * 4 + (size_t)a.max_bias * 12;
+    const int per = (slices + LG_RANGES - 1) / LG_RANGES;
+    auto go = [&](auto kern) {
+        const cudaError_t e = set_smem(kern, TILE * 4 + kMaxLogitBias * 12);
+        return e != cudaSuccess ? e : launch_ex(kern, grid, dim3(LG_THREADS), smem, c2, 1, a, per);
+    };
+    if (a.max_history <= kLogitsUnsorted)
+        return a.mask ? go(logits_kernel<T, TILE, true, false, true>) : go(logits_kernel<T, TILE, true, false, false>);
+    const cudaError_t e = launch_ex(logits_sort_kernel<T, TILE>, dim3(a.rows), dim3(LG_SORT), 0, c2, 1, a, per);
+    if (e != cudaSuccess)
+        return e;
+    c2.pdl = true;   // waits for the sort itself
+    return a.mask ? go(logits_kernel<T, TILE, true, true, true>) : go(logits_kernel<T, TILE, true, true, false>);
 }
 
 template <class T>
 cudaError_t launch_t(const LogitsArgs &a, const LaunchCfg &c)
 {
-    const size_t smem = LG_TILE * 4 + (size_t)a.max_bias * 12;
-    cudaError_t e = set_smem(logits_kernel<T>, LG_TILE * 4 + kMaxLogitBias * 12);
-    if (e != cudaSuccess)
-        return e;
-    LaunchCfg c2 = c;
-    c2.pdl = false;
-    return launch_ex(logits_kernel<T>, dim3((a.vocab + LG_TILE - 1) / LG_TILE, a.rows), dim3(LG_THREADS), smem,
-                     c2, 1, a);
+    // slices of 16 KB, unless that would leave SMs without one
+    constexpr int TILE = 16384 / (int)sizeof(typename Elem<T>::raw);
+    if ((long long)a.rows * ((a.vocab + TILE - 1) / TILE) >= 2 * c.num_sms)
+        return launch_tile<T, TILE>(a, c);
+    return launch_tile<T, 2048>(a, c);
 }
 
 }  // namespace
 
-cudaError_t launch_logits(const LogitsArgs &a, int dtype, const LaunchCfg &c)
+size_t logits_workspace_bytes(int rows, int max_history)
 {
+    if (max_history <= kLogitsUnsorted)
+        return 0;
+    return align_up((size_t)rows * (LG_RANGES + 1) * 4, 16) + (size_t)rows * max_history * 4;
+}
+
+cudaError_t launch_logits(const LogitsArgs &args, int dtype, void *ws, const LaunchCfg &c)
+{
+    LogitsArgs a = args;
+    a.begin = static_cast<int *>(ws);
+    a.sorted = reinterpret_cast<int *>(static_cast<char *>(ws) + align_up((size_t)a.rows * (LG_RANGES + 1) * 4, 16));
     return dtype == QMOE_F32 ? launch_t<float>(a, c)
            : dtype == QMOE_BF16 ? launch_t<__nv_bfloat16>(a, c) : launch_t<__half>(a, c);
 }

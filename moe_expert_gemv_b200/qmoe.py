@@ -8,6 +8,7 @@ A non-zero status raises QmoeError.  There is no CPU fallback: if the library
 is missing or the device is not an sm_100 GPU the calls fail loudly.
 """
 import ctypes
+import functools
 import os
 import struct
 
@@ -89,7 +90,8 @@ def lib():
             "kv_append": [p, p, p, p, p, p, i32, p, p, p, p],
             "attn_paged_workspace_bytes": [i32, i64],
             "attn_paged": [p, p, p, p, sz, p, p],
-            "logits_process": [p, p, i64, i32, i32, i32, p, i64, p, p],
+            "logits_process": [p, p, i64, i32, i32, i32, p, i64, p, sz, p, p],
+            "logits_process_workspace_bytes": [i32, i32],
             "qmoe_pack_codes": [p, i32, i32, i32, p, p],
             "qmoe_unpack_codes": [p, i32, i32, i32, p, p],
             "qmoe_check_status": [p, p, p],
@@ -118,6 +120,7 @@ def lib():
         L.moe_decode_workspace_bytes.restype = sz
         L.moe_decode_pack_bytes.restype = sz
         L.attn_paged_workspace_bytes.restype = sz
+        L.logits_process_workspace_bytes.restype = sz
         L.qmoe_status_string.restype = ctypes.c_char_p
         L.qmoe_version.restype = i32
         L.qmoe_set_dependent_launch.restype = i32
@@ -962,8 +965,16 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
 
 
 # --------------------------------------------------------- rules on logits --
+_logits_ws = {}   # one workspace for each device and stream
+
+
+@functools.lru_cache(maxsize=None)
+def _logits_need(rows, max_history):
+    return lib().logits_process_workspace_bytes(rows, max_history)
+
+
 def logits_process(logits, out=None, history=None, history_len=None, prompt_len=None, repetition=None,
-                   presence=None, frequency=None, bias_ids=None, bias=None, mask=None, status=None):
+                   presence=None, frequency=None, bias_ids=None, bias=None, mask=None, workspace=None, status=None):
     """Penalties, biases and a grammar mask on logits [rows][vocab] (float16,
     bfloat16 or float32); out may be logits itself.  history int32 [rows][n]
     with history_len int32 [rows] tokens in use, prompt_len of them the prompt;
@@ -1013,8 +1024,21 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
                     _opt(bias, torch.float32, "bias", (R, max_bias), dev), mask_ptr, mask_stride, max_hist, max_bias)
     if R == 0 or V == 0:   # empty tensors have no address
         return out
+    ws = nbytes = 0
+    need = _logits_need(R, max_hist)
+    if workspace is not None:
+        ws, nbytes = _on(dev, workspace, "workspace").data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        key = (dev.index, _raw_stream(dev))
+        held = None if torch.cuda.is_current_stream_capturing() else _logits_ws.get(key)
+        if held is None or held.numel() < need:
+            held = torch.empty(need, dtype=torch.uint8, device=dev)
+            if not torch.cuda.is_current_stream_capturing():   # a capture's stays with its graph
+                _logits_ws[key] = held
+        ws, nbytes = held.data_ptr(), held.numel()
     _device_call(lib().logits_process, "logits_process", dev, c, logits.data_ptr(), logits.stride(0) if R > 1 else V,
-                 _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0) if R > 1 else V, _status(status, dev))
+                 _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0) if R > 1 else V, ws, nbytes,
+                 _status(status, dev))
     return out
 
 

@@ -139,17 +139,21 @@ def test_logits_refusals():
     full = dict(history=PTR, history_len=PTR, prompt_len=PTR, history_stride=8, repetition=PTR, presence=PTR, frequency=PTR,
                 bias_ids=PTR, bias=PTR, mask=PTR, mask_stride=4, max_history=8, max_bias=3)
 
-    def call(x=PTR, ist=100, dtype=2, rows=2, vocab=100, out=PTR, ost=100, **kw):
-        return L.logits_process(ctypes.byref(qmoe.CLogitRules(**(full | kw))), x, ist, dtype, rows, vocab, out, ost, None, None)
+    def call(x=PTR, ist=100, dtype=2, rows=2, vocab=100, out=PTR, ost=100, ws=PTR, nbytes=1 << 30, **kw):
+        return L.logits_process(ctypes.byref(qmoe.CLogitRules(**(full | kw))), x, ist, dtype, rows, vocab, out, ost, ws, nbytes, None, None)
 
     for kw, code in [(dict(x=None), INVALID), (dict(out=None), INVALID), (dict(dtype=3), INVALID), (dict(rows=-1), INVALID),
                      (dict(vocab=0), INVALID), (dict(ist=99), INVALID), (dict(ost=99), INVALID), (dict(history_len=None), INVALID),
                      (dict(history=None), INVALID), (dict(history=None, max_history=0), INVALID), (dict(history_stride=7), INVALID),
                      (dict(mask_stride=3), INVALID), (dict(bias=None), INVALID), (dict(max_bias=-1), INVALID), (dict(rows=65536), UNSUP),
                      (dict(max_bias=1025), UNSUP), (dict(max_history=1 << 20, history_stride=1 << 20), UNSUP), (dict(x=PTR + 2), ALIGN),
-                     (dict(mask=PTR + 2), ALIGN), (dict(bias=PTR + 1), ALIGN)]:
+                     (dict(mask=PTR + 2), ALIGN), (dict(bias=PTR + 1), ALIGN), (dict(ws=PTR + 8), ALIGN),
+                     (dict(max_history=9000, history_stride=9000, ws=None), WS),
+                     (dict(max_history=9000, history_stride=9000, nbytes=1000), WS)]:
         assert call(**kw) == code, kw
-    assert L.logits_process(None, PTR, 100, 2, 2, 100, PTR, 100, None, None) == INVALID
+    assert L.logits_process(None, PTR, 100, 2, 2, 100, PTR, 100, None, 0, None, None) == INVALID
+    need = L.logits_process_workspace_bytes
+    assert need(0, 100) == need(5, -1) == need(5, 100) == 0 and need(5, 9000) > 5 * 9000 * 4 and need(6, 9000) > need(5, 9000)
 
 
 def test_struct_sizes_match_the_header(tmp_path):

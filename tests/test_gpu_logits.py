@@ -185,3 +185,36 @@ def test_python_refusals(cuda_dev):
     with pytest.raises(qmoe.QmoeError):
         qmoe.logits_process(x, bias_ids=torch.zeros(2, 1025, dtype=torch.int32, device="cuda"),
                             bias=torch.zeros(2, 1025, device="cuda"))
+
+
+def test_more_tokens_than_a_table_holds(cuda_dev):
+    """Long histories of tokens that all differ, and ones whose hashes fall
+    together (the table's parts go by the low 16 bits of 0x9E3779B1 * id)."""
+    V = 200000
+    part = [i for i in range(V) if ((i * 0x9E3779B1 & 0xFFFF) * 4 >> 16) == 1]
+    assert len(part) > 12000
+    for ids in (torch.randperm(V)[:60000], torch.tensor(part[:12000]), torch.tensor(part[:12000]).repeat(2)):
+        d = make(1, V, len(ids), 5, True, seed=3)
+        d["history"], d["history_len"] = ids[None].int(), torch.tensor([len(ids)], dtype=torch.int32)
+        d["prompt_len"] = torch.tensor([len(ids) // 3], dtype=torch.int32)
+        check(d, run(d))
+
+
+def test_captured_and_replayed_with_new_rules(cuda_dev):
+    d = make(3, 40000, 900, 4, True, torch.bfloat16)
+    c = {k: v.cuda() for k, v in d.items()}
+    x = c.pop("logits")
+    out = torch.empty_like(x)
+    qmoe.logits_process(x, out=out, **c)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qmoe.logits_process(x, out=out, **c)
+    for seed in (1, 2):
+        d = make(3, 40000, 900, 4, True, torch.bfloat16, seed=seed)
+        x.copy_(d["logits"])
+        for k in c:
+            c[k].copy_(d[k])
+        g.replay()
+        torch.cuda.synchronize()
+        check(d, out)
+    assert qmoe.qmoe_check_status() == 0
