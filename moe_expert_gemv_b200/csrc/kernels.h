@@ -294,6 +294,7 @@ struct RopeArgs {
     long long page_stride, token_stride, head_stride;
     int batch, tokens, heads, kv_heads, dim, rot, interleaved;
     int page_size, num_pages, max_pages;
+    FastDiv by_unit, by_v, by_page;
     float scale;
     int32_t *status;
 };
