@@ -596,9 +596,10 @@ qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
  * Scores, softmax statistics and sums are fp32; a weight enters the second
  * product rounded to the cache's type, the output is rounded once.
  * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device
- * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every call
- * leaves its counters zero again, so calls of any shape share it in turn, but
- * not two that can run at the same time.  max_rows: the most rows of one
+ * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every
+ * call leaves them zero again (but for one that raised QMOE_DEV_TIMEOUT: zero
+ * them then), so calls of any shape share it in turn, but not two that can run
+ * at the same time.  max_rows: the most rows of one
  * sequence per K/V head in any call, max_new * heads / kv_heads (max_new 0:
  * take `tokens`).
  * UNSUPPORTED: head_dim not a multiple of 8 or above 256; tokens * heads / kv_heads
@@ -642,6 +643,8 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
  * workspace: logits_process_workspace_bytes(rows, max_history) bytes of device
  * memory, 16-byte aligned, no initial contents required, not used by two calls
  * that can run at the same time; 0 (and NULL allowed) for short histories.
+ * UNSUPPORTED: rows above 65535, vocab above 2^26, max_history from 2^20 on,
+ * max_bias above 1024.
  * ------------------------------------------------------------------------- */
 typedef struct qmoe_logit_rules {
     const int32_t *history;
