@@ -743,7 +743,14 @@ def _opt(t, dtype, what, shape, device):
         raise TypeError("%s must be a %s tensor" % (what, dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous and have shape %s" % (what, tuple(shape)))
-    return _on(device, t, what).data_ptr()
+    if t.device != device:
+        _on(device, t, what)
+    return t.data_ptr()
+
+
+def _new_like(x):
+    """A contiguous tensor of x's shape and type (torch.empty costs twice as much)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _status(t, device):
@@ -855,7 +862,7 @@ def rope_rotate(rope, x, positions, out=None, status=None):
         raise TypeError("x must be a float16 or bfloat16 tensor [tokens][heads][dim]")
     dev = _on(rope.device, x, "x").device
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _new_like(x)
     x_ptr, x_token, x_head = _rows(x, "x", x.dtype, dev, x.shape)
     o_ptr, o_token, o_head = _rows(out, "out", x.dtype, dev, x.shape)
     T, H, D = x.shape
@@ -887,7 +894,7 @@ def kv_append(cache, batch, k, v, q=None, rope=None, positions=None, q_out=None,
         shape = (T, heads, cache.head_dim)
         cq = _pack_rows(*_rows(q, "q", dt, dev, shape))
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dt, device=dev)
+            q_out = _new_like(q)
         co = _pack_rows(*_rows(q_out, "q_out", dt, dev, shape))
     if T == 0:   # empty tensors have no address
         return q_out
@@ -945,7 +952,7 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
     shape = (T, H, cache.head_dim)
     q_ptr, q_token, q_head = _rows(q, "q", cache.dtype, dev, shape)
     if out is None:
-        out = torch.empty(shape, dtype=cache.dtype, device=dev)
+        out = _new_like(q)
         o_ptr, o_token, o_head = out.data_ptr(), H * D, D
     else:
         o_ptr, o_token, o_head = _rows(out, "out", cache.dtype, dev, shape)
@@ -985,12 +992,15 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
         raise TypeError("logits must be a CUDA tensor [rows][vocab] of float16, bfloat16 or float32")
     R, V = logits.shape
     dev = logits.device
+    in_stride, step = logits.stride()
     if out is None:
-        out = torch.empty(R, V, dtype=logits.dtype, device=dev)
-    if out.dtype != logits.dtype or out.shape != logits.shape:
-        raise ValueError("out must be like logits")
-    _on(dev, out, "out")
-    if V > 1 and (logits.stride(1) != 1 or out.stride(1) != 1):
+        out, out_stride = _new_like(logits), V
+    else:
+        if out.dtype != logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must be like logits")
+        out_stride, out_step = _on(dev, out, "out").stride()
+        step = 1 if step == out_step == 1 else 0
+    if V > 1 and step != 1:
         raise ValueError("a row's logits must follow each other")
     hist = hist_stride = max_hist = mask_ptr = mask_stride = max_bias = 0
     if history is not None:
@@ -1001,6 +1011,9 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
             raise ValueError("history needs history_len")
         max_hist = history.shape[1]
         hist, hist_stride = _on(dev, history, "history").data_ptr(), history.stride(0) if R > 1 else max_hist
+        if max_hist == 0:   # nothing written yet (and an empty tensor has no address): no penalties
+            history_len = prompt_len = repetition = presence = frequency = None
+            hist = hist_stride = 0
     elif any(t is not None for t in (history_len, prompt_len, repetition, presence, frequency)):
         raise ValueError("penalties need history")
     if (bias_ids is None) != (bias is None):
@@ -1036,8 +1049,8 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
             if not torch.cuda.is_current_stream_capturing():   # a capture's stays with its graph
                 _logits_ws[key] = held
         ws, nbytes = held.data_ptr(), held.numel()
-    _device_call(lib().logits_process, "logits_process", dev, c, logits.data_ptr(), logits.stride(0) if R > 1 else V,
-                 _DTYPES[logits.dtype], R, V, out.data_ptr(), out.stride(0) if R > 1 else V, ws, nbytes,
+    _device_call(lib().logits_process, "logits_process", dev, c, logits.data_ptr(), in_stride if R > 1 else V,
+                 _DTYPES[logits.dtype], R, V, out.data_ptr(), out_stride if R > 1 else V, ws, nbytes,
                  _status(status, dev))
     return out
 

@@ -218,3 +218,20 @@ def test_captured_and_replayed_with_new_rules(cuda_dev):
         torch.cuda.synchronize()
         check(d, out)
     assert qmoe.qmoe_check_status() == 0
+
+
+def test_no_history_yet(cuda_dev):
+    """A history without columns is none; a row's logits have to be apart from each other."""
+    x = torch.randn(3, 70, device="cuda")
+    none = torch.empty(3, 0, dtype=torch.int32, device="cuda")
+    y = qmoe.logits_process(x, history=none, history_len=torch.zeros(3, dtype=torch.int32, device="cuda"),
+                            repetition=torch.full((3,), 2.0, device="cuda"))
+    assert torch.equal(y, x)
+    for bad in (x[:, :1].expand(3, 70), x.t().contiguous().t()):
+        with pytest.raises(ValueError):
+            qmoe.logits_process(bad)
+        with pytest.raises(ValueError):
+            qmoe.logits_process(bad, out=torch.empty_like(x))
+    with pytest.raises(ValueError):
+        qmoe.logits_process(x, out=x[:, :1].expand(3, 70))
+    assert qmoe.qmoe_check_status() == 0
