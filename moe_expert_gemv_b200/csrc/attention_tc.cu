@@ -248,6 +248,14 @@ __device__ __forceinline__ TcShared *tc_shared(const AttnArgs &a)
     return reinterpret_cast<TcShared *>(a.part + (size_t)kAttnMaxSms * 2 * M * (DP + 2));
 }
 
+// Where in a part four sums lie, columns 4u.. of row r: a thread that holds a
+// row and a warp that holds 32 of them both go through memory in order.
+template <int M>
+__device__ __forceinline__ int tc_at(int u, int r)
+{
+    return (u * M + r) * 4;
+}
+
 // Keys that every row of a block sees: [lo_max, hi_min).
 __device__ __forceinline__ void at_limits(const AttnArgs &a, const AttnSeq &s, int row0, int rows, int &lo_max,
                                           int &hi_min)
@@ -339,6 +347,12 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                      "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == W_MMA + 1 && lane == 0 && a.tma) {   // fetched while the lengths are
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+        if (a.tma_q)
+            prefetch_tensormap(&maps.q);
     }
     pdl_trigger();   // the joining kernel may be launched; it waits for this one's end
     const AttnSpan span = attn_span<M, KT, TC_EX>(a);
@@ -532,24 +546,36 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 unsigned char *v = smem + C::v_off + stage * C::tile;
                 const int r1 = min(max(lo_max - j0, 0), KT), r2 = max(min(hi_min - j0, KT), r1);
                 const int c = t % CPR;
+                const int n = KT - (r2 - r1), step = nt / CPR, lo = w.lo, hi = w.hi;
                 if (c < cpr)
-                    for (int i = t / CPR; i < KT - (r2 - r1); i += nt / CPR) {
-                        const int r = i < r1 ? i : i + (r2 - r1), j = j0 + r;
-                        uint4 *q = reinterpret_cast<uint4 *>(v + at_sw(KT, r, c));
-                        if (j < w.lo || j >= w.hi) {
-                            *q = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 x = *q;
-                        if (nonfinite2<T>(x.x) || nonfinite2<T>(x.y) || nonfinite2<T>(x.z) || nonfinite2<T>(x.w)) {
-                            uint32_t *p = reinterpret_cast<uint32_t *>(&x);
+                    for (int i0 = t / CPR; i0 < n; i0 += 4 * step) {
+                        uint4 x[4];   // four rows' loads are under way at once
+                        int r[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = Num16<T>::up2(p[k]);
-                                p[k] = Num16<T>::down2(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = i0 + k * step;
+                            r[k] = i < n ? (i < r1 ? i : i + (r2 - r1)) : -1;
+                            if (r[k] >= 0)
+                                x[k] = *reinterpret_cast<const uint4 *>(v + at_sw(KT, r[k], c));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (r[k] < 0)
+                                continue;
+                            uint4 *q = reinterpret_cast<uint4 *>(v + at_sw(KT, r[k], c));
+                            if (j0 + r[k] < lo || j0 + r[k] >= hi) {
+                                *q = make_uint4(0, 0, 0, 0);
+                            } else if (nonfinite2<T>(x[k].x) || nonfinite2<T>(x[k].y) || nonfinite2<T>(x[k].z) ||
+                                       nonfinite2<T>(x[k].w)) {
+                                uint32_t *p = reinterpret_cast<uint32_t *>(&x[k]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = Num16<T>::up2(p[e]);
+                                    p[e] = Num16<T>::down2(isfinite(f.x) ? f.x : 0.f, isfinite(f.y) ? f.y : 0.f);
+                                }
+                                *q = x[k];
+                                *poison = 1;
                             }
-                            *q = x;
-                            *poison = 1;
                         }
                     }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -588,36 +614,28 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     if (*poison != 0)
                         at_restore<T, Walk, KT>(a, w, row0, rows, rr, to);
                     const int tok = a.by_group(row0 + rr), hq = w.h * a.group + (row0 + rr) - tok * a.group;
-                    // where this lane's row goes, in bytes; others are told by shuffle
-                    const long long mine = whole ? ((w.s.q0 + tok) * a.o_token + hq * a.o_head) * 2
-                                                 : (long long)rr * DP * 4;
-                    char *const dst = whole ? reinterpret_cast<char *>(a.out) : reinterpret_cast<char *>(part);
-                    const float inv = mlr.y == 0.f ? 0.f : 1.f / mlr.y;
-                    const int unit = lane & 7, step = whole ? 64 : 32;   // columns of 128 bytes
-                    // x[i]: the 16 rows' units of 16 bytes this lane writes to shared memory
-                    auto store = [&](int part16, int c0) {
-                        __syncwarp();
-                        uint4 x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 4 + (lane >> 3);
-                            x[i] = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((unit ^ (r & 7)) << 4));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = part16 * 16 + i * 4 + (lane >> 3);
-                            const long long at = __shfl_sync(0xffffffffu, mine, r);
-                            if (r0 + r < rows && c0 + unit * (step / 8) < a.dim)
-                                *reinterpret_cast<uint4 *>(dst + at + c0 * (128 / step) + unit * 16) = x[i];
-                        }
-                        __syncwarp();
-                    };
+                    if (!whole) {
 #pragma unroll 1
-                    for (int c0 = 0; c0 < a.dim; c0 += step) {
-                        uint32_t v[32];
-                        at_ld32(to + c0, v);
-                        at_wait_ld(v);
-                        if (whole) {
+                        for (int c0 = 0; c0 < a.dim; c0 += 32) {
+                            uint32_t v[32];
+                            at_ld32(to + c0, v);
+                            at_wait_ld(v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (rr < rows && c0 + i * 4 < a.dim)
+                                    *reinterpret_cast<uint4 *>(part + tc_at<M>(c0 / 4 + i, rr)) =
+                                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        }
+                    } else {
+                        // where this lane's row goes; the others are told by shuffle
+                        const long long mine = (w.s.q0 + tok) * a.o_token + hq * a.o_head;
+                        const float inv = mlr.y == 0.f ? 0.f : 1.f / mlr.y;
+                        const int unit = lane & 7;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < a.dim; c0 += 64) {
+                            uint32_t v[32];
+                            at_ld32(to + c0, v);
+                            at_wait_ld(v);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 v[i] = Num16<T>::down2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
@@ -630,16 +648,30 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                                     v[16 + i] = Num16<T>::down2(__uint_as_float(u[2 * i]) * inv,
                                                                 __uint_as_float(u[2 * i + 1]) * inv);
                             }
-                        }
 #pragma unroll
-                        for (int part16 = 0; part16 < 2; ++part16) {
-                            if ((lane >> 4) == part16) {
+                            for (int half = 0; half < 2; ++half) {
+                                if ((lane >> 4) == half) {
 #pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    *reinterpret_cast<uint4 *>(stg + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                                        make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                                    for (int i = 0; i < 8; ++i)
+                                        *reinterpret_cast<uint4 *>(stg + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                                            make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                                }
+                                __syncwarp();
+                                uint4 x[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int r = i * 4 + (lane >> 3);
+                                    x[i] = *reinterpret_cast<const uint4 *>(stg + r * 128 + ((unit ^ (r & 7)) << 4));
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int r = half * 16 + i * 4 + (lane >> 3);
+                                    const long long at = __shfl_sync(0xffffffffu, mine, r);
+                                    if (r0 + r < rows && c0 + unit * 8 < a.dim)
+                                        *reinterpret_cast<uint4 *>(a.out + at + c0 + unit * 8) = x[i];
+                                }
+                                __syncwarp();
                             }
-                            store(part16, c0);
                         }
                     }
                     at_fence_before();
@@ -663,8 +695,6 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 const uint32_t bytes = KT * 128 * nblk;
                 const void *map = x ? &maps.v : &maps.k;
                 uint32_t n = 0;   // tiles so far
-                if (lane == 0 && a.tma && x < 2)
-                    prefetch_tensormap(map);
                 for (; a.tma && x < 2 && !w.done() && !dead; advance()) {
                     const int ta = w.ta(), tb = w.tb();
                     int j = (w.t0 + ta) * KT + lane * a.tma;
@@ -704,8 +734,6 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 if (x == 2 && a.tma_q) {
                     // ---- the query rows: 128 rows are 128 / group tokens x the group's heads
                     uint32_t un = 0;
-                    if (lane == 0)
-                        prefetch_tensormap(&maps.q);
                     for (; !w.done() && !dead; advance(), ++un) {
                         const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
                         const int nr = NROW == 2 && rows > 128 ? 2 : 1;
@@ -925,28 +953,6 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     at_fence_after();
                     const uint32_t ts = tq + C::s_col + buf * 128;
                     const bool cut = __any_sync(0xffffffffu, l0 > 0 || h0 < KT);
-                    if (a.softcap > 0.f || cut) {
-                        // caps and masks, in tensor memory (kept short: they would
-                        // be most of the code)
-                        const float capc = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : 0.f;
-#pragma unroll 1
-                        for (int c = 0; c < KT; c += 32) {
-                            uint32_t x[32];
-                            at_ld32(ts + c, x);
-                            at_wait_ld(x);
-                            if (a.softcap > 0.f) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    x[i] = __float_as_uint(capped(__uint_as_float(x[i]), capc, a.softcap * kLog2e));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < l0 || c + i >= h0)
-                                    x[i] = 0xFF800000u;   // -inf
-                            at_st32(ts + c, x);
-                        }
-                        at_wait_st();
-                    }
                     uint32_t s[KT];
 #pragma unroll
                     for (int c = 0; c < KT; c += 32)
@@ -955,6 +961,24 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
 #pragma unroll
                     for (int c = 32; c < KT; c += 32)
                         at_pin(s + c);
+                    if (a.softcap > 0.f) {
+                        const float capc = a.scale * 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            s[c] = __float_as_uint(capped(__uint_as_float(s[c]), capc, cap));
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int c = 0; c < KT; c += 32) {
+                            // of 32 keys the row sees those from lo on and below hi
+                            const int lo = min(max(l0 - c, 0), 32), hi = min(max(h0 - c, 0), 32);
+                            const uint32_t see = (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1))
+                                    s[c + i] = 0xFF800000u;   // -inf
+                        }
+                    }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int c = 0; c < KT; c += 2)
@@ -1029,21 +1053,73 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     }
 }
 
-// Joins the parts of the units that several CTAs shared: CTA (x, y) takes 8
-// rows of the unit that begins in CTA x, a warp a row (32 rows a CTA, four to a
-// warp in turn, took 12.5 us where this takes 5: a row is two rounds of loads).
-constexpr int TJ_ROWS = 8, TJ_THREADS = 256;
+// Joins the parts of the units that several CTAs shared.  CTA (x, y) takes 32
+// rows and 64 columns of the unit that begins in CTA x: a lane a row, a warp 8
+// columns, so that reads are whole lines; 8 parts' loads are under way at once.
+constexpr int TJ_THREADS = 256, TJ_PARTS = 8;
 
 template <class T, int DP, int M>
 __global__ void __launch_bounds__(TJ_THREADS) attn_join_kernel(const AttnArgs a)
 {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r0 = (int)blockIdx.y % (M / 32) * 32, r = r0 + lane;
+    const int u = ((int)blockIdx.y / (M / 32) * 8 + warp) * 2;   // columns 4u.. of 8
     pdl_wait();
     const TcShared d = tc_shared<M, DP>(a)[blockIdx.x];
-    if (d.c1 == 0)
+    if (d.c1 == 0 || r0 >= d.rows || u * 4 >= a.dim)
         return;
-    const int r1 = min((int)blockIdx.y * TJ_ROWS + TJ_ROWS, d.rows);
-    for (int r = blockIdx.y * TJ_ROWS + (threadIdx.x >> 5); r < r1; r += TJ_THREADS / 32)
-        attn_join_row<T, M, DP, 8>(a, blockIdx.x, d.c1, r, d.q0, d.row0 + r, d.h);
+    const int np = d.c1 - (int)blockIdx.x + 1;
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    for (int k0 = 0; k0 < np; k0 += TJ_PARTS) {
+        float mk[TJ_PARTS], lk[TJ_PARTS];
+        float4 v[TJ_PARTS][2];
+#pragma unroll
+        for (int x = 0; x < TJ_PARTS; ++x) {
+            const int k = k0 + x;
+            const float *p = attn_part<M, DP>(a, blockIdx.x + k, k == 0);
+            mk[x] = -INFINITY;
+            lk[x] = 0.f;
+            v[x][0] = v[x][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < np) {
+                mk[x] = __ldcg(p + M * DP + r);
+                lk[x] = __ldcg(p + M * DP + M + r);
+                v[x][0] = __ldcg(reinterpret_cast<const float4 *>(p + tc_at<M>(u, r)));
+                v[x][1] = __ldcg(reinterpret_cast<const float4 *>(p + tc_at<M>(u + 1, r)));
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int x = 0; x < TJ_PARTS; ++x)
+            top = fmaxf(top, mk[x]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = exp2_approx(m - base);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] *= f;
+#pragma unroll
+        for (int x = 0; x < TJ_PARTS; ++x) {   // in the parts' order
+            const float w = exp2_approx(mk[x] - base);
+            l += w * lk[x];
+            const float *vx = reinterpret_cast<const float *>(v[x]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] += w * vx[i];
+        }
+    }
+    if (r >= d.rows)
+        return;
+    const int tok = a.by_group(d.row0 + r), hq = d.h * a.group + d.row0 + r - tok * a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        out[i] = Num16<T>::down2(o[2 * i] * inv, o[2 * i + 1] * inv);
+    *reinterpret_cast<uint4 *>(a.out + (d.q0 + tok) * a.o_token + hq * a.o_head + u * 4) =
+        make_uint4(out[0], out[1], out[2], out[3]);
+    if (u == 0 && a.lse)
+        a.lse[(size_t)(d.q0 + tok) * a.heads + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <class T, int DP, int NROW>
@@ -1073,7 +1149,7 @@ cudaError_t launch_tc(const AttnArgs &args, const LaunchCfg &c)
         return e;
     // always as a dependent: it waits for the parts itself
     c2.pdl = true;
-    return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / TJ_ROWS), dim3(TJ_THREADS), 0, c2, 1, a);
+    return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / 32 * (DP / 64)), dim3(TJ_THREADS), 0, c2, 1, a);
 }
 
 template <class T>
