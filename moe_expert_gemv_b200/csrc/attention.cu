@@ -106,6 +106,12 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
         flag[1] = 0;
         *abort_word = 0;
     }
+    if (TMA && tid == AM_THREADS) {   // fetched while the lengths are
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+    }
+    pdl_wait();
+    pdl_trigger();
     AttnWalk<M, AM_KT, AM_EX> w;
     w.start(a, attn_span<M, AM_KT, AM_EX>(a));
     __syncthreads();
@@ -118,8 +124,6 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
         const void *map = x ? &maps.v : &maps.k;
         uint32_t n = 0;
         bool dead = false;
-        if (bx == 0)
-            prefetch_tensormap(map);
         for (; !w.done() && !dead; w.next(a)) {
             const int tb = w.tb();
             int j = (w.t0 + w.ta()) * AM_KT + bx * a.tma;
@@ -492,9 +496,7 @@ cudaError_t launch_rows(const AttnArgs &a, const AttnMaps &maps, const LaunchCfg
         return e;
     constexpr int per_sm = DP == 256 ? 1 : 2;
     static_assert(per_sm * (L::total + 1024) <= 228 * 1024 && per_sm <= 3, "shared memory");
-    LaunchCfg c2 = c;
-    c2.pdl = false;
-    return launch_ex(kern, dim3(c.num_sms * per_sm), dim3(AM_THREADS + (TMA ? 32 : 0)), L::total, c2, 1, a, maps);
+    return launch_ex(kern, dim3(c.num_sms * per_sm), dim3(AM_THREADS + (TMA ? 32 : 0)), L::total, c, 1, a, maps);
 }
 
 template <class T>

@@ -319,7 +319,6 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
     constexpr int W_MMA = C::SOFT / 32;
 
     if (tid == 0) {
-        tc_shared<M, DP>(a)[blockIdx.x].c1 = 0;
         const int full = a.tma ? 1 : C::LOAD;
         mbar_init(&bar[TB_QF], a.tma_q ? 1 : C::LOAD);
         mbar_init(&bar[TB_QE], 1);
@@ -354,7 +353,10 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
         if (a.tma_q)
             prefetch_tensormap(&maps.q);
     }
+    pdl_wait();
     pdl_trigger();   // the joining kernel may be launched; it waits for this one's end
+    if (tid == 0)
+        tc_shared<M, DP>(a)[blockIdx.x].c1 = 0;
     const AttnSpan span = attn_span<M, KT, TC_EX>(a);
     at_fence_before();
     __syncthreads();
@@ -1065,6 +1067,7 @@ __global__ void __launch_bounds__(TJ_THREADS) attn_join_kernel(const AttnArgs a)
     const int r0 = (int)blockIdx.y % (M / 32) * 32, r = r0 + lane;
     const int u = ((int)blockIdx.y / (M / 32) * 8 + warp) * 2;   // columns 4u.. of 8
     pdl_wait();
+    pdl_trigger();
     const TcShared d = tc_shared<M, DP>(a)[blockIdx.x];
     if (d.c1 == 0 || r0 >= d.rows || u * 4 >= a.dim)
         return;
@@ -1142,12 +1145,11 @@ cudaError_t launch_tc(const AttnArgs &args, const LaunchCfg &c)
     cudaError_t e = set_smem(kern, C::total);
     if (e != cudaSuccess)
         return e;
-    LaunchCfg c2 = c;
-    c2.pdl = false;
-    e = launch_ex(kern, dim3(c.num_sms), dim3(C::THREADS), C::total, c2, 1, a, maps);
+    e = launch_ex(kern, dim3(c.num_sms), dim3(C::THREADS), C::total, c, 1, a, maps);
     if (e != cudaSuccess)
         return e;
     // always as a dependent: it waits for the parts itself
+    LaunchCfg c2 = c;
     c2.pdl = true;
     return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / 32 * (DP / 64)), dim3(TJ_THREADS), 0, c2, 1, a);
 }

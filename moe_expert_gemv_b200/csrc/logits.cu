@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(LG_SORT) logits_sort_kernel(const LogitsArgs a
     constexpr int NW = LG_SORT / 32, NC = LG_RANGES * NW, KEEP = 12;
     __shared__ int cnt[NC];   // [range][warp]
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_trigger();
+    pdl_wait();
+    pdl_trigger();   // after the wait: the next kernel reads the logits at once
     const int n = min(max(a.history_len[row], 0), a.max_history);
     const int p = a.prompt_len ? a.prompt_len[row] : 0;
     const int32_t *h = a.history + row * a.history_stride;
@@ -219,6 +220,10 @@ __global__ void __launch_bounds__(LG_THREADS, 5) logits_kernel(const LogitsArgs 
     if (v0 >= a.vocab)
         return;
     const bool vec_out = reinterpret_cast<uintptr_t>(out - shift) % 16 == 0;
+    if (!SORTED) {   // with a sort before, that has waited
+        pdl_wait();
+        pdl_trigger();
+    }
     union Vec {
         uint4 q;
         uint32_t w[4];
@@ -418,7 +423,6 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
     using R = typename Elem<T>::raw;
     const int slices = (int)((a.vocab + 16 / (long long)sizeof(R) - 1 + TILE - 1) / TILE);
     LaunchCfg c2 = c;
-    c2.pdl = false;
     const dim3 grid(a.rows, slices);
     if (a.max_history == 0 && a.max_bias == 0)
         return a.mask ? launch_ex(logits_kernel<T, TILE, false, false, true>, grid, dim3(LG_THREADS), 0, c2, 1, a, 1)

@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(RP_THREADS) rope_kernel(const RopeArgs a)
 {
     extern __shared__ __align__(16) float2 cs[];   // [rot / 2, rounded up to even] m cos, m sin
     const int t = blockIdx.x, tid = threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
     const int half = a.rot >> 1;
     // units of a head: the rotated part's pairs of 8 (half layout: first-half
     // unit with its partner; interleaved: one unit), then the copied rest
@@ -239,11 +241,9 @@ cudaError_t launch_t(const RopeArgs &args, const LaunchCfg &c)
                      al(a.q, a.q_token, a.q_head) && al(a.q_out, a.qo_token, a.qo_head) &&
                      al(a.k, a.k_token, a.k_head) && al(a.v, a.v_token, a.v_head) &&
                      al(a.ck, a.token_stride, a.head_stride) && al(a.cv, a.page_stride, 0);
-    LaunchCfg c2 = c;
-    c2.pdl = false;
     const size_t smem = (size_t)(a.rot / 2 + 1) / 2 * 16;
     auto kern = vec ? rope_kernel<T, true> : rope_kernel<T, false>;
-    return launch_ex(kern, dim3(a.tokens), dim3(RP_THREADS), smem, c2, 1, a);
+    return launch_ex(kern, dim3(a.tokens), dim3(RP_THREADS), smem, c, 1, a);
 }
 
 }  // namespace
