@@ -17,12 +17,13 @@
 // whoever takes the word out (an exchange with zero) writes the token -- few
 // threads with a token each, where a look at every word by the thread that
 // holds the logit sends whole warps through the rules for one lane (109 us
-// instead of 93 for this kernel alone on the case below).  A token that no rule touches leaves
-// as the bits it came.  Counting is integer, so the order of the atomics does
-// not show.
-// A short history is looked through by every slice.  A long one is first
-// sorted by ranges of slices, in a kernel of a CTA per row that the slices'
-// kernel overlaps (its logits do not wait for it).  Measured, 256 x 262144
+// instead of 93 for this kernel alone on the case below).  A token that no rule
+// touches leaves as the bits it came.  Counting is integer, so the order of the
+// atomics does not show.
+// A short history is looked through by every slice.  Where that is much work
+// (launch_tile) it is first sorted by ranges of slices, in a kernel of a CTA
+// per row that the slices' kernel overlaps (its logits do not wait for it).
+// Measured, 256 x 262144
 // bf16 with histories of up to 12000 tokens, a mask (44 us without a history,
 // which is 6.4 TB/s): 92 us.  There the looking through unsorted histories
 // took 112 us, a full sort by slice 106 us; tokens counted in hash tables and
@@ -433,7 +434,13 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
         const cudaError_t e = set_smem(kern, TILE * 4 + kMaxLogitBias * 12);
         return e != cudaSuccess ? e : launch_ex(kern, grid, dim3(LG_THREADS), smem, c2, 1, a, per);
     };
-    if (a.max_history <= kLogitsUnsorted)
+    // Looking through a history takes each slice its length.  Measured (fp16),
+    // looking through unsorted and sorted histories: 256 rows of
+    // 262144 with 1024 tokens 51 and 55 us, 2048 66 and 61, 4096 92 and 70, 8192
+    // 149 and 86; 48 of 151937 with 8192 27 and 26 (fp32, twice the slices, 4096:
+    // 23 and 21 with biases and a mask); one of 32000 with 4096 10 and 15, 8192
+    // 17 and 23.
+    if (a.max_history <= kLogitsUnsorted || (long long)a.rows * slices * a.max_history < 7000000)
         return a.mask ? go(logits_kernel<T, TILE, true, false, true>) : go(logits_kernel<T, TILE, true, false, false>);
     const cudaError_t e = launch_ex(logits_sort_kernel<T, TILE>, dim3(a.rows), dim3(LG_SORT), 0, c2, 1, a, per);
     if (e != cudaSuccess)

@@ -235,3 +235,24 @@ def test_no_history_yet(cuda_dev):
     with pytest.raises(ValueError):
         qmoe.logits_process(x, out=x[:, :1].expand(3, 70))
     assert qmoe.qmoe_check_status() == 0
+
+
+@pytest.mark.parametrize("rows,vocab,hist,dtype,mask", [(8, 262144, 33000, torch.float16, False), (300, 60001, 4000, torch.bfloat16, True),
+                                                        (1, 70001, (1 << 20) - 1, torch.float32, True),
+                                                        (17, 200003, 22000, torch.float32, False)])
+def test_much_work_with_histories(cuda_dev, rows, vocab, hist, dtype, mask):
+    """Histories long enough, over rows and vocabulary, to be sorted first."""
+    d = make(rows, vocab, hist, biases=5, mask=mask, dtype=dtype, seed=rows)
+    g = torch.Generator().manual_seed(1)
+    d["history"][torch.rand(d["history"].shape, generator=g) < 0.1] = -1
+    if rows > 2:
+        d["history_len"][1], d["history_len"][2] = 0, 1
+    y = run(d)
+    check(d, y)
+    assert torch.equal(y, run(d))
+    c = d["logits"].cuda()
+    x = {k: v.cuda() for k, v in d.items() if k != "logits"}
+    assert torch.equal(qmoe.logits_process(c, out=c, **x), y)
+    x["history"][0, 0] = vocab
+    qmoe.logits_process(c, **x)
+    assert qmoe.qmoe_check_status() == qmoe.DEV_BAD_TOKEN
