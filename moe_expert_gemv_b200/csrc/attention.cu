@@ -10,12 +10,16 @@
 // registers.  Up to 16 query rows; 4 warps share a tile's 64 keys (each with
 // its own maximum and sum, joined at the end of a unit), products on mma.sync
 // m16n8k16 with the rows padded to 16 -- a 128-row tcgen05 tile would hold
-// 120 empty rows, and a step of it costs a warpgroup's round trip through
-// tensor memory (64 sequences of up to 4K tokens: see launch_attn).
+// 112 empty rows or more, and a step of it costs a warpgroup's round trip
+// through tensor memory.
 // A producer warp brings K and V by TMA, a box of up to a page each, into a
 // ring of stages that runs on into the next unit; caches without a tensor map
 // (see attn_maps) are read by the four warps with 16-byte cp.async from
-// wherever the page table says.
+// wherever the page table says.  Measured: 64 ragged sequences of up to 4096
+// tokens, 8 K/V heads of 128 (529 MB), 93 us, 5.7 TB/s; 2 of 100000, 4 K/V
+// heads (410 MB), 81 us, 5.1 TB/s (a plain reduction of as many bytes takes
+// 86); 2 of 400000, 6.3 TB/s; one of 900, 10 us, which is latency: lengths,
+// page table, cache, the joining of 16 CTAs' parts, one after the other.
 #include "attn.cuh"
 
 namespace qmoe {
@@ -23,8 +27,10 @@ namespace {
 
 constexpr int AM_THREADS = 128;
 constexpr int AM_KT = 64;
-constexpr int AM_EX = 1;         // beginning and ending a unit, in tiles
-constexpr int AM_ROWS = 16;      // more rows than this go to tcgen05
+// Beginning and ending a unit, in tiles: 512 units of 2 to 64 tiles take 105 us
+// with 0, 98 with 1, 93 with 3, 97 with 9.
+constexpr int AM_EX = 3;
+constexpr int AM_ROWS = 16;      // more rows than this go to tcgen05 (launch_attn)
 constexpr float AM_LAZY = 8.f;   // log2 of the growth of a maximum that sums are not rescaled for
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
@@ -602,8 +608,14 @@ cudaError_t launch_attn(const AttnArgs &a, bool bf16, long long max_rows, const 
 {
     if (c.num_sms > kAttnMaxSms)
         return cudaErrorInvalidValue;
+    // Measured, this kernel and the tcgen05 one: 4 rows, 64 sequences of up to
+    // 4096 tokens, 98 and 125 us, one of 900, 12 and 17; 8 rows of heads of 64,
+    // 63 and 100; 16 rows 64 and 67; 32 rows (two blocks of 16 read everything
+    // twice) 59 and 45; 48 rows 75 and 37.
     if (max_rows > AM_ROWS)
-        // two row tiles per unit once there are units for every SM
+        // two row tiles per unit once there are units for every SM: 4 chunks of
+        // 2048 tokens take 344 us with two, 423 with one; a chunk of 512, 62 both
+        // ways; of 128, 37 with two, 31 with one
         return launch_attn_tc(a, bf16, (long long)a.tokens * a.group / 256 * a.kv_heads >= c.num_sms ? 2 : 1, c);
     return bf16 ? launch_dim<__nv_bfloat16>(a, true, c) : launch_dim<__half>(a, false, c);
 }
