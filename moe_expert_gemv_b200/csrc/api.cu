@@ -4,7 +4,7 @@
 // The operations and where the pages define them are listed in qmoe.h.  This
 // layer allocates nothing and never synchronises inside a compute call; the
 // one per-device object it owns is a status word in a __device__ variable.
-#include <math.h>
+#include <cmath>
 
 #include <atomic>
 #include <mutex>
@@ -963,7 +963,7 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     if (s != QMOE_OK)
         return s;
     if (attn->heads < 1 || attn->heads % cache->kv_heads || attn->window < 0 || !(attn->softcap >= 0.f) ||
-        !(attn->scale > 0.f))
+        !(attn->scale > 0.f) || std::isinf(attn->softcap) || std::isinf(attn->scale))
         return QMOE_ERR_INVALID_ARG;
     const int group = attn->heads / cache->kv_heads;
     if ((long long)batch->tokens * group > (1ll << 30) || (long long)batch->tokens * attn->heads > (1ll << 31))

@@ -1163,10 +1163,7 @@ cudaError_t launch_tc(const AttnArgs &args, const LaunchCfg &c)
     e = launch_ex(kern, dim3(c.num_sms), dim3(C::THREADS), C::total, c, 1, a, maps);
     if (e != cudaSuccess)
         return e;
-    // always as a dependent: it waits for the parts itself
-    LaunchCfg c2 = c;
-    c2.pdl = true;
-    return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / 32 * (DP / 64)), dim3(TJ_THREADS), 0, c2, 1, a);
+    return launch_ex(attn_join_kernel<T, DP, C::M>, dim3(c.num_sms, C::M / 32 * (DP / 64)), dim3(TJ_THREADS), 0, c, 1, a);
 }
 
 template <class T>

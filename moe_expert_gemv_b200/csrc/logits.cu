@@ -423,16 +423,15 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
 {
     using R = typename Elem<T>::raw;
     const int slices = (int)((a.vocab + 16 / (long long)sizeof(R) - 1 + TILE - 1) / TILE);
-    LaunchCfg c2 = c;
     const dim3 grid(a.rows, slices);
     if (a.max_history == 0 && a.max_bias == 0)
-        return a.mask ? launch_ex(logits_kernel<T, TILE, false, false, true>, grid, dim3(LG_THREADS), 0, c2, 1, a, 1)
-                      : launch_ex(logits_kernel<T, TILE, false, false, false>, grid, dim3(LG_THREADS), 0, c2, 1, a, 1);
+        return a.mask ? launch_ex(logits_kernel<T, TILE, false, false, true>, grid, dim3(LG_THREADS), 0, c, 1, a, 1)
+                      : launch_ex(logits_kernel<T, TILE, false, false, false>, grid, dim3(LG_THREADS), 0, c, 1, a, 1);
     const size_t smem = TILE * 4 + (size_t)a.max_bias * 12;
     const int per = (slices + LG_RANGES - 1) / LG_RANGES;
     auto go = [&](auto kern) {
         const cudaError_t e = set_smem(kern, TILE * 4 + kMaxLogitBias * 12);
-        return e != cudaSuccess ? e : launch_ex(kern, grid, dim3(LG_THREADS), smem, c2, 1, a, per);
+        return e != cudaSuccess ? e : launch_ex(kern, grid, dim3(LG_THREADS), smem, c, 1, a, per);
     };
     // Looking through a history takes each slice its length.  Measured (fp16),
     // looking through unsorted and sorted histories: 256 rows of
@@ -442,10 +441,9 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
     // 17 and 23.
     if (a.max_history <= kLogitsUnsorted || (long long)a.rows * slices * a.max_history < 7000000)
         return a.mask ? go(logits_kernel<T, TILE, true, false, true>) : go(logits_kernel<T, TILE, true, false, false>);
-    const cudaError_t e = launch_ex(logits_sort_kernel<T, TILE>, dim3(a.rows), dim3(LG_SORT), 0, c2, 1, a, per);
+    const cudaError_t e = launch_ex(logits_sort_kernel<T, TILE>, dim3(a.rows), dim3(LG_SORT), 0, c, 1, a, per);
     if (e != cudaSuccess)
         return e;
-    c2.pdl = true;   // waits for the sort itself
     return a.mask ? go(logits_kernel<T, TILE, true, true, true>) : go(logits_kernel<T, TILE, true, true, false>);
 }
 

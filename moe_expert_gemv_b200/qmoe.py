@@ -739,18 +739,18 @@ def _opt(t, dtype, what, shape, device):
     """Address of an optional contiguous tensor (None: 0)."""
     if t is None:
         return 0
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError("%s must be a %s tensor" % (what, dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous and have shape %s" % (what, tuple(shape)))
-    if t.device != device:
+    if t.get_device() != device.index:
         _on(device, t, what)
     return t.data_ptr()
 
 
 def _new_like(x):
     """A contiguous tensor of x's shape and type (torch.empty costs twice as much)."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _status(t, device):
@@ -761,7 +761,7 @@ def _status(t, device):
 def _rows(t, what, dtype, device, shape):
     """Address, token and head stride of a [tokens][heads][dim] tensor of any
     token and head strides."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device.index:
         raise TypeError("%s must be a %s tensor on %s" % (what, dtype, device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
@@ -820,12 +820,12 @@ class KVBatch:
 
     def _c(self, tokens):
         """Address of the C struct for steps of `tokens` rows."""
-        c = self._by_tokens.get(tokens)
-        if c is None:
+        held = self._by_tokens.get(tokens)
+        if held is None:
             c = CKVBatch(self.page_table.data_ptr(), self.q_start.data_ptr(), self.kv_len.data_ptr(),
                          self.page_table.shape[0], self.page_table.shape[1], tokens, self.max_new)
-            self._by_tokens[tokens] = c
-        return ctypes.addressof(c)
+            held = self._by_tokens[tokens] = (ctypes.addressof(c), c)
+        return held[0]
 
 
 def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, trained=0, low=1.0, high=4.0):

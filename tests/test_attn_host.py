@@ -174,3 +174,8 @@ def test_struct_sizes_match_the_header(tmp_path):
     got = list(map(int, subprocess.run([str(tmp_path / "sizes")], stdout=subprocess.PIPE, check=True).stdout.split()))
     want = [x for c in names.values() for x in [ctypes.sizeof(c)] + [getattr(c, f[0]).offset for f in c._fields_]]
     assert got == want
+
+
+def test_attention_refuses_infinite_factors():
+    for kw in (dict(softcap=math.inf), dict(scale=math.inf)):
+        assert attn(cache(), batch(), **kw) == INVALID

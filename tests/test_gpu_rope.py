@@ -152,3 +152,23 @@ def test_python_refusals(cuda_dev):
         qmoe.kv_append(c.cache, c.batch(), k, k, rope=qmoe.Rope.make(66))
     with pytest.raises(TypeError):
         qmoe.rope_rotate(qmoe.Rope.make(64), k, torch.zeros(1, dtype=torch.int64, device="cuda"))
+
+
+def test_append_many_sequences_in_place(cuda_dev):
+    """More sequences than two steps of a warp's search tell apart, some without new tokens; q turned where it lies."""
+    g = torch.Generator().manual_seed(2)
+    n = torch.randint(0, 3, (1300,), generator=g)
+    kv = n + torch.randint(0, 20, (1300,), generator=g)
+    n[0] = kv[0] = 0
+    c = Case(list(zip(n.tolist(), kv.tolist())), 4, 1, 64, 8, seed=5)
+    T = c.tokens
+    r = qmoe.Rope.make(64)
+    q, k = torch.randn(T, 4, 64, device="cuda").half(), torch.randn(T, 1, 64, device="cuda").half()
+    pos = torch.cat([torch.arange(b - a, b) for a, b in c.lens]).int().cuda()
+    want_q, want_k = qmoe.rope_rotate(r, q, pos), qmoe.rope_rotate(r, k, pos)
+    y = q.clone()
+    assert qmoe.kv_append(c.cache, c.batch(), k, k, q=y, rope=r, q_out=y) is y
+    assert qmoe.qmoe_check_status() == 0 and torch.equal(y, want_q)
+    pg = torch.cat([s[0][b - a:] for (a, b), s in zip(c.lens, c.slots)])
+    sl = torch.cat([s[1][b - a:] for (a, b), s in zip(c.lens, c.slots)])
+    assert torch.equal(c.k[pg, sl], want_k) and torch.equal(c.v[pg, sl], k)

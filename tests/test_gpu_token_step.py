@@ -144,3 +144,24 @@ def test_replayed_step(cuda_dev):
             assert torch.equal(want[k], got[k]), "%s, step %d" % (k, i)
         check_step(m, b, got)
     assert int(status) == 0 and qmoe.qmoe_check_status() == 0
+
+
+@pytest.mark.parametrize("lens", [[(1, 900), (1, 3)], [(40, 700), (128, 128)]])
+def test_without_dependent_launches(cuda_dev, lens):
+    """The same bits with and without programmatic dependent launches."""
+    rows = torch.randn(300, 60001, device="cuda").half()
+    hist = torch.randint(0, 60001, (300, 4000), dtype=torch.int32, device="cuda")
+    rules = dict(history=hist, history_len=torch.full((300,), 4000, dtype=torch.int32, device="cuda"),
+                 frequency=torch.ones(300, device="cuda"))
+    got = []
+    for on in (1, 0):
+        before = qmoe.qmoe_set_dependent_launch(on)
+        try:
+            c = State(lens, 8).case
+            k = torch.randn(c.tokens, KV, DIM, generator=torch.Generator().manual_seed(1)).half().cuda()
+            q = qmoe.kv_append(c.cache, c.batch(), k, k, q=c.q, rope=qmoe.Rope.make(ROT))
+            got.append((q, qmoe.attn_paged(c.cache, c.batch(), q), qmoe.logits_process(rows, **rules)))
+            torch.cuda.synchronize()
+        finally:
+            qmoe.qmoe_set_dependent_launch(before)
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and qmoe.qmoe_check_status() == 0
