@@ -23,9 +23,10 @@
 // A short history is looked through by every slice.  Where that is much work
 // (launch_tile) it is first sorted by ranges of slices, in a kernel of a CTA
 // per row that the slices' kernel overlaps (its logits do not wait for it).
-// Measured, 256 x 262144
-// bf16 with histories of up to 12000 tokens, a mask (44 us without a history,
-// which is 6.4 TB/s): 92 us.  There the looking through unsorted histories
+// Measured, 256 x 262144 bf16 with histories of up to 12000 tokens, a mask: 90
+// us (44 without a history, which is 6.4 TB/s), of which the sort is the first
+// 15; then a slice's chain of loads (its range, its tokens, their logits) takes
+// 5 us, and 5 CTAs fit on an SM.  There the looking through unsorted histories
 // took 112 us, a full sort by slice 106 us; tokens counted in hash tables and
 // written by a second kernel 87 us, but 7.6 us instead of 4.2 for one short
 // row; a cluster's CTAs counting into one another's words 238 us (texts repeat
@@ -43,7 +44,7 @@ constexpr int LG_BIAS_SHIFT = 20;             // 11 bits: 1 + index of the first
 constexpr uint32_t LG_COUNT = (1u << LG_BIAS_SHIFT) - 1;
 constexpr int LG_THREADS = 256;
 constexpr int LG_RANGES = 8;                  // ranges of slices that a history is sorted by
-constexpr int LG_SORT = 1024;                 // threads of the sort
+constexpr int LG_SORT = 512;                  // threads of the sort: two CTAs on an SM
 
 template <class T>
 struct Elem;
@@ -77,15 +78,20 @@ __device__ __forceinline__ int row_shift(const LogitsArgs &a, int row)
 // slices (the sign bit: behind the prompt), a.begin[row][r] where range r's
 // begin.  So each slice looks through its own range's tokens; 8 ranges leave
 // at most an eighth more of them than a sort by slice, which costs more than
-// that (31 us instead of 18, 256 rows of up to 12000 tokens).  Counting
-// sort: the lanes of a warp whose tokens fall into one range take their places
-// together, from a counter of the warp's own.
-template <class T, int TILE>
-__global__ void __launch_bounds__(LG_SORT) logits_sort_kernel(const LogitsArgs a, int per)
+// that.  Counting sort, LG_CHUNK tokens at a time: a thread's counts of the 8
+// ranges are 16-bit fields of two words, scanned over the CTA, after which it
+// knows its tokens' places; they go there in shared memory and from there to
+// the row in order.
+constexpr int LG_KEEP = 24, LG_CHUNK = LG_KEEP * LG_SORT;   // tokens a thread, and at a time
+static_assert(LG_RANGES == 8 && LG_CHUNK < 65536, "fields");
+
+template <class T>
+__global__ void __launch_bounds__(LG_SORT, 2) logits_sort_kernel(const LogitsArgs a, const FastDiv by_range)
 {
     using R = typename Elem<T>::raw;
-    constexpr int NW = LG_SORT / 32, NC = LG_RANGES * NW, KEEP = 12;
-    __shared__ int cnt[NC];   // [range][warp]
+    extern __shared__ __align__(16) int placed[];   // [LG_CHUNK]
+    __shared__ unsigned long long warps[LG_SORT / 32][2], all[2];
+    __shared__ int place[LG_RANGES];   // where the ranges' next tokens go
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();   // after the wait: the next kernel reads the logits at once
@@ -94,104 +100,124 @@ __global__ void __launch_bounds__(LG_SORT) logits_sort_kernel(const LogitsArgs a
     const int32_t *h = a.history + row * a.history_stride;
     int *out = a.sorted + (size_t)row * a.max_history;
     const int shift = row_shift<R>(a, row);
-    const float inv = 1.f / (float)(TILE * per);
-    if (tid < NC)
-        cnt[tid] = 0;
-    __syncthreads();
-    // place of this lane's token within its (range, warp); -1: not a token
-    auto take = [&](int id, int &r) {
-        const bool ok = (unsigned)id < (unsigned)a.vocab;
-        // a range more or less by rounding at a border would be wrong: settled in integers
-        r = ok ? (int)((float)(id + shift) * inv) : LG_RANGES;
-        if (ok) {
-            r -= r * (TILE * per) > id + shift;
-            r += (r + 1) * (TILE * per) <= id + shift;
-        }
-        unsigned peers = 0xffffffffu;
+    int id[LG_KEEP];
+    unsigned long long c[2];
+    auto field = [](const unsigned long long *f, int r) { return (int)((r < 4 ? f[0] : f[1]) >> (16 * (r & 3)) & 0xFFFF); };
+    auto range = [&](int id) { return (int)by_range((uint32_t)(id + shift)); };
+    auto count = [&](int i0) {   // tokens i0.. of the row: ids (-1: none) and this thread's counts
+        c[0] = c[1] = 0;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {   // r <= 8
-            const unsigned ones = __ballot_sync(0xffffffffu, (r >> b) & 1);
-            peers &= (r >> b) & 1 ? ones : ~ones;
+        for (int k = 0; k < LG_KEEP; ++k)
+            id[k] = i0 + k * LG_SORT + tid < n ? __ldg(h + i0 + k * LG_SORT + tid) : -1;
+#pragma unroll
+        for (int k = 0; k < LG_KEEP; ++k) {
+            if ((unsigned)id[k] >= (unsigned)a.vocab) {
+                if (id[k] != -1)
+                    flag_status(a.status, QMOE_DEV_BAD_TOKEN);
+                id[k] = -1;
+                continue;
+            }
+            const int r = range(id[k]);
+            c[0] += r < 4 ? 1ull << (16 * r) : 0;
+            c[1] += r < 4 ? 0 : 1ull << (16 * (r - 4));
         }
-        const int lead = __ffs(peers) - 1;
-        int at = 0;
-        if (lane == lead && ok) {
-            at = cnt[r * NW + warp];
-            cnt[r * NW + warp] = at + __popc(peers);
-        }
-        __syncwarp();
-        at = __shfl_sync(0xffffffffu, at, lead) + __popc(peers & ((1u << lane) - 1));
-        if (!ok && id != -1)
-            flag_status(a.status, QMOE_DEV_BAD_TOKEN);
-        return ok ? at : -1;
     };
-    int id[KEEP], at[KEEP], r[KEEP];   // the first tokens' stay in registers
+    // counts of the threads before this one; `all`: of the chunk
+    auto scan = [&]() {
+        unsigned long long s[2] = {c[0], c[1]};
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        id[k] = k * LG_SORT + tid < n ? __ldg(h + k * LG_SORT + tid) : -1;
+        for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k) {
-        at[k] = -1;
-        if (k * LG_SORT < n)
-            at[k] = take(id[k], r[k]);
-    }
-    for (int i = KEEP * LG_SORT; i < n; i += LG_SORT) {
-        int x;
-        take(i + tid < n ? __ldg(h + i + tid) : -1, x);
-    }
-    __syncthreads();
-    if (warp == 0) {   // counts to places
-        int sum = 0;
-#pragma unroll
-        for (int k = 0; k < LG_RANGES; ++k) {
-            const int c = cnt[k * NW + lane];
-            int incl = c;
+            for (int x = 0; x < 2; ++x) {
+                const unsigned long long u = __shfl_up_sync(0xffffffffu, s[x], o);
+                s[x] += lane >= o ? u : 0;
+            }
+        if (lane == 31) {
+            warps[warp][0] = s[0];
+            warps[warp][1] = s[1];
+        }
+        __syncthreads();
+        if (warp < 2) {   // a word each
+            const unsigned long long mine = lane < LG_SORT / 32 ? warps[lane][warp] : 0;
+            unsigned long long t = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += u;
+                const unsigned long long u = __shfl_up_sync(0xffffffffu, t, o);
+                t += lane >= o ? u : 0;
             }
-            cnt[k * NW + lane] = sum + incl - c;
-            if (lane == 0)
-                a.begin[(size_t)row * (LG_RANGES + 1) + k] = sum;
-            sum += __shfl_sync(0xffffffffu, incl, 31);
+            if (lane < LG_SORT / 32)
+                warps[lane][warp] = t - mine;
+            if (lane == 31)
+                all[warp] = t;
         }
-        if (lane == 0)
-            a.begin[(size_t)row * (LG_RANGES + 1) + LG_RANGES] = sum;
-    }
-    __syncthreads();
-    auto put = [&](int i, int id, int r, int at) {
-        out[cnt[r * NW + warp] + at] = i >= p ? id | (int)0x80000000 : id;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            c[x] = s[x] - c[x] + warps[warp][x];
     };
-    int first[LG_RANGES];   // the warp's places that the kept tokens have taken
-#pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        if (at[k] >= 0)
-            put(k * LG_SORT + tid, id[k], r[k], at[k]);
-    if (n > KEEP * LG_SORT) {
-        // the rest once more: their places follow on the kept ones'
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < LG_RANGES; ++k) {
-            int c = 0;
-#pragma unroll
-            for (int j = 0; j < KEEP; ++j)
-                c += __popc(__ballot_sync(0xffffffffu, at[j] >= 0 && r[j] == k));
-            first[k] = c;
+    if (tid < LG_RANGES)
+        place[tid] = 0;
+    if (n > LG_CHUNK) {   // the ranges' sizes first
+        for (int i0 = 0; i0 < n; i0 += LG_CHUNK) {
+            count(i0);
+            scan();
+            if (tid < LG_RANGES)
+                place[tid] += field(all, tid);
         }
-        __syncwarp();
-        if (lane == 0)
+        __syncthreads();
+    }
+    for (int i0 = 0; i0 == 0 || i0 < n; i0 += LG_CHUNK) {
+        count(i0);
+        scan();
+        if (i0 == 0) {
+            if (tid == 0) {
+                int sum = 0;
+                for (int r = 0; r < LG_RANGES; ++r) {
+                    const int size = n > LG_CHUNK ? place[r] : field(all, r);
+                    a.begin[(size_t)row * (LG_RANGES + 1) + r] = place[r] = sum;
+                    sum += size;
+                }
+                a.begin[(size_t)row * (LG_RANGES + 1) + LG_RANGES] = sum;
+            }
+        }
+        int first[LG_RANGES + 1];   // of the ranges, in the chunk
+        first[0] = 0;
 #pragma unroll
-            for (int k = 0; k < LG_RANGES; ++k)
-                cnt[k * NW + warp] += first[k];
-        __syncwarp();
-        for (int i = KEEP * LG_SORT; i < n; i += LG_SORT) {
-            int x;
-            const int y = i + tid < n ? __ldg(h + i + tid) : -1;
-            const int z = take(y, x);   // counts on from the warp's places
-            if (z >= 0)
-                out[z] = i + tid >= p ? y | (int)0x80000000 : y;
+        for (int r = 0; r < LG_RANGES; ++r)
+            first[r + 1] = first[r] + field(all, r);
+        // this thread's next places in the chunk: the fields' sums fit 16 bits
+#pragma unroll
+        for (int r = 0; r < LG_RANGES; ++r)
+            c[r >> 2] += (unsigned long long)first[r] << (16 * (r & 3));
+#pragma unroll
+        for (int k = 0; k < LG_KEEP; ++k)
+            if (id[k] >= 0) {
+                const int r = range(id[k]);
+                placed[field(c, r)] = i0 + k * LG_SORT + tid >= p ? id[k] | (int)0x80000000 : id[k];
+                c[0] += r < 4 ? 1ull << (16 * r) : 0;
+                c[1] += r < 4 ? 0 : 1ull << (16 * (r - 4));
+            }
+        __syncthreads();
+        for (int i = tid; i < first[LG_RANGES]; i += LG_SORT) {
+            int at = i;
+            if (n > LG_CHUNK) {
+                int r = 0;
+#pragma unroll
+                for (int x = 1; x < LG_RANGES; ++x)
+                    r += i >= first[x];
+                int f = 0;
+#pragma unroll
+                for (int x = 1; x < LG_RANGES; ++x)
+                    f = r == x ? first[x] : f;
+                at = place[r] + i - f;
+            }
+            out[at] = placed[i];
+        }
+        if (n > LG_CHUNK) {
+            __syncthreads();
+            if (tid < LG_RANGES)
+                place[tid] += field(all, tid);
+            __syncthreads();
         }
     }
 }
@@ -435,13 +461,16 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
     };
     // Looking through a history takes each slice its length.  Measured (fp16),
     // looking through unsorted and sorted histories: 256 rows of
-    // 262144 with 1024 tokens 51 and 55 us, 2048 66 and 61, 4096 92 and 70, 8192
-    // 149 and 86; 48 of 151937 with 8192 27 and 26 (fp32, twice the slices, 4096:
+    // 262144 with 1024 tokens 51 and 55 us, 2048 66 and 61, 4096 92 and 68, 8192
+    // 149 and 82; 48 of 151937 with 8192 27 and 25 (fp32, twice the slices, 4096:
     // 23 and 21 with biases and a mask); one of 32000 with 4096 10 and 15, 8192
     // 17 and 23.
     if (a.max_history <= kLogitsUnsorted || (long long)a.rows * slices * a.max_history < 7000000)
         return a.mask ? go(logits_kernel<T, TILE, true, false, true>) : go(logits_kernel<T, TILE, true, false, false>);
-    const cudaError_t e = launch_ex(logits_sort_kernel<T, TILE>, dim3(a.rows), dim3(LG_SORT), 0, c, 1, a, per);
+    constexpr size_t chunk = LG_CHUNK * 4;
+    cudaError_t e = set_smem(logits_sort_kernel<T>, chunk);
+    if (e == cudaSuccess)
+        e = launch_ex(logits_sort_kernel<T>, dim3(a.rows), dim3(LG_SORT), chunk, c, 1, a, FastDiv((uint32_t)(TILE * per)));
     if (e != cudaSuccess)
         return e;
     return a.mask ? go(logits_kernel<T, TILE, true, true, true>) : go(logits_kernel<T, TILE, true, true, false>);
