@@ -222,3 +222,68 @@ def test_python_refusals(cuda_dev):
         qmoe.attn_paged(c.cache, b, c.q.cpu())
     with pytest.raises(ValueError):
         qmoe.KVCache(c.k, c.v[:-1])
+
+
+# enough rows for two row tiles in a unit
+MANY = [(300, 700), (70, 70), (1, 33), (0, 40), (230, 257), (40, 40), (5, 0)]
+
+
+def many(c):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert c.q.shape[0] * (c.heads // c.kv_heads) // 256 * c.kv_heads >= sms
+    return c
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(64, 8), (62, 2), (64, 1)])
+@pytest.mark.parametrize("dim,page,dtype", [(128, 16, BF16), (128, 7, F16), (64, 64, F16), (104, 32, BF16), (80, 1, F16), (8, 16, F16)])
+def test_two_row_tiles(cuda_dev, heads, kv_heads, dim, page, dtype):
+    c = many(Case(MANY, heads, kv_heads, dim, page, dtype, seed=dim, spare=3))
+    out = torch.full(c.q.shape, 7.0, dtype=dtype, device="cuda")
+    lse = torch.full(c.q.shape[:2], 7.0, device="cuda")
+    run(c, 300, out=out, lse=lse)
+    c.check(out, lse)
+    assert (out[c.tokens:] == 7).all() and (lse[c.tokens:] == 7).all()
+    again = torch.empty_like(out)
+    run(c, 300, out=again)
+    assert torch.equal(again[:c.tokens], out[:c.tokens])
+
+
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=100), dict(cap=5.0), dict(cap=50.0, window=200), dict(causal=False),
+                                dict(causal=False, window=30, cap=9.0)], ids=str)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_two_row_tiles_with_masks_and_caps(cuda_dev, kw, dim):
+    c = many(Case(MANY, 64, 8, dim, 16, seed=7))
+    out, lse = run(c, 300, **kw)
+    c.check(out, lse, **kw)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 7), (128, 64)])
+def test_two_row_tiles_with_poison(cuda_dev, bad, dim, page):
+    c = many(Case([(300, 330), (300, 310), (30, 90)], 64, 8, dim, page, BF16))
+    for b, j in ((0, 326), (0, 150), (1, 20), (1, 300), (2, 70)):
+        c.values[b][j, :, ::3] = bad
+    c.write()
+    for kw in (dict(), dict(window=60)):
+        out, lse = run(c, 300, **kw)
+        c.check(out, lse, **kw)
+
+
+def test_two_row_tiles_in_a_graph(cuda_dev):
+    c = many(Case(MANY[:-1], 64, 8, 128, 16))
+    b = c.batch(300)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        out, lse = qmoe.attn_paged(c.cache, b, c.q, want_lse=True)
+    keys, values = c.keys, c.values
+    for cut in (0, 37):
+        c.lens = [(n, max(kv - cut, n)) for n, kv in MANY[:-1]]
+        c.kv_len.copy_(torch.tensor([kv for _, kv in c.lens], dtype=torch.int32))
+        c.keys = [k[:kv] for k, (_, kv) in zip(keys, c.lens)]
+        c.values = [v[:kv] for v, (_, kv) in zip(values, c.lens)]
+        g.replay()
+        torch.cuda.synchronize()
+        c.check(out, lse)
+    assert qmoe.qmoe_check_status() == 0
