@@ -256,3 +256,16 @@ def test_much_work_with_histories(cuda_dev, rows, vocab, hist, dtype, mask):
     x["history"][0, 0] = vocab
     qmoe.logits_process(c, **x)
     assert qmoe.qmoe_check_status() == qmoe.DEV_BAD_TOKEN
+
+
+@pytest.mark.parametrize("dtype", list(STEP))
+@pytest.mark.parametrize("hist,biases,mask", [(1500, 9, True), (300, 0, False), (0, 30, True), (0, 0, True), (0, 0, False)])
+def test_large_slices(cuda_dev, dtype, hist, biases, mask):
+    """Rows enough for slices of 16 KB, which begin anywhere within 16 bytes."""
+    d = make(48, 60001, hist, biases, mask, dtype, seed=hist + biases)
+    y = run(d)
+    check(d, y)
+    out = torch.full((48, 60007), 7.0, dtype=dtype, device="cuda")
+    c = {k: v.cuda() for k, v in d.items()}
+    qmoe.logits_process(c.pop("logits"), out=out[:, 3:60004], **c)
+    assert torch.equal(out[:, 3:60004], y) and (out[:, :3] == 7).all() and (out[:, 60004:] == 7).all()
