@@ -223,6 +223,14 @@ __global__ void __launch_bounds__(LG_SORT, 2) logits_sort_kernel(const LogitsArg
 }
 
 // ------------------------------------------------------------------ slices --
+// bit 7 of lo in every bit of the lower half, bit 15 of hi in every one of the upper
+__device__ __forceinline__ uint32_t halves(uint32_t lo, uint32_t hi)
+{
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, 0xDD88;" : "=r"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
 // CTA (row, t): TILE places of the row; slices later than rows in the grid's
 // order, because a text's tokens crowd in the first slices and those should
 // not come last.  WORDS: there is a history or a bias;
@@ -365,8 +373,7 @@ __global__ void __launch_bounds__(LG_THREADS, 5) logits_kernel(const LogitsArgs 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // an element's bit becomes a mask of its width
-                    const uint32_t keep = E == 4 ? 0u - ((m >> j) & 1u)
-                                                 : ((m >> (2 * j)) & 1u) * 0xFFFFu | ((m >> (2 * j + 1)) & 1u) * 0xFFFF0000u;
+                    const uint32_t keep = E == 4 ? 0u - ((m >> j) & 1u) : halves(m << (7 - 2 * j), m << (14 - 2 * j));
                     x[k].w[j] = (x[k].w[j] & keep) | (Elem<T>::none & ~keep);
                 }
             }
