@@ -23,7 +23,7 @@
 // A short history is looked through by every slice.  Where that is much work
 // (launch_tile) it is first sorted by ranges of slices, in a kernel of a CTA
 // per row that the slices' kernel overlaps (its logits do not wait for it).
-// Measured, 256 x 262144 bf16 with histories of up to 12000 tokens, a mask: 90
+// Measured, 256 x 262144 bf16 with histories of up to 12000 tokens, a mask: 88
 // us (44 without a history, which is 6.4 TB/s), of which the sort is the first
 // 15; then a slice's chain of loads (its range, its tokens, their logits) takes
 // 5 us, and 5 CTAs fit on an SM.  There the looking through unsorted histories
@@ -462,10 +462,8 @@ cudaError_t launch_tile(const LogitsArgs &a, const LaunchCfg &c)
                       : launch_ex(logits_kernel<T, TILE, false, false, false>, grid, dim3(LG_THREADS), 0, c, 1, a, 1);
     const size_t smem = TILE * 4 + (size_t)a.max_bias * 12;
     const int per = (slices + LG_RANGES - 1) / LG_RANGES;
-    auto go = [&](auto kern) {
-        const cudaError_t e = set_smem(kern, TILE * 4 + kMaxLogitBias * 12);
-        return e != cudaSuccess ? e : launch_ex(kern, grid, dim3(LG_THREADS), smem, c, 1, a, per);
-    };
+    static_assert(TILE * 4 + kMaxLogitBias * 12 <= 48 * 1024, "shared memory without asking for more");
+    auto go = [&](auto kern) { return launch_ex(kern, grid, dim3(LG_THREADS), smem, c, 1, a, per); };
     // Looking through a history takes each slice its length.  Measured (fp16),
     // looking through unsorted and sorted histories: 256 rows of
     // 262144 with 1024 tokens 51 and 55 us, 2048 66 and 61, 4096 92 and 68, 8192
