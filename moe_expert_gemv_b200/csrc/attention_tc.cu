@@ -563,7 +563,10 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 unsigned char *v = smem + C::v_off + stage * C::tile;
                 const int r1 = min(max(lo_max - j0, 0), KT), r2 = max(min(hi_min - j0, KT), r1);
                 const int c = t % CPR;
-                const int n = KT - (r2 - r1), step = nt / CPR, lo = w.lo, hi = w.hi;
+                const int step = nt / CPR, lo = w.lo, hi = w.hi;
+                // The rows at the limits one after the other; without TMA each thread
+                // stays with those its own cp.async brings: it has waited for no others.
+                const int n = a.tma ? KT - (r2 - r1) : KT;
                 if (c < cpr)
                     for (int i0 = t / CPR; i0 < n; i0 += 4 * step) {
                         uint4 x[4];   // four rows' loads are under way at once
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int i = i0 + k * step;
-                            r[k] = i < n ? (i < r1 ? i : i + (r2 - r1)) : -1;
+                            r[k] = i >= n ? -1 : i < r1 ? i : a.tma ? i + (r2 - r1) : i >= r2 ? i : -1;
                             if (r[k] >= 0)
                                 x[k] = *reinterpret_cast<const uint4 *>(v + at_sw(KT, r[k], c));
                         }

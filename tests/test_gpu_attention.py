@@ -1,6 +1,7 @@
 """attn_paged against the formula in 64 bits: types, head layouts, page sizes,
 lengths from none to long ones, masks, poison where nothing may be read."""
 import math
+import threading
 
 import pytest
 import torch
@@ -287,3 +288,46 @@ def test_two_row_tiles_in_a_graph(cuda_dev):
         torch.cuda.synchronize()
         c.check(out, lse)
     assert qmoe.qmoe_check_status() == 0
+
+
+def test_two_threads_on_one_stream(cuda_dev):
+    """Calls of two kernels each, with one workspace, from two threads at once."""
+    cases = [Case([(60, 4000)], 8, 2, 128, 16, seed=1), Case([(200, 3000)], 8, 2, 128, 16, seed=2)]
+    want = [qmoe.attn_paged(c.cache, c.batch(), c.q) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            for _ in range(200):
+                got[i].append(qmoe.attn_paged(cases[i].cache, cases[i].batch(), cases[i].q))
+        except Exception as e:  # shown by the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and qmoe.qmoe_check_status() == 0
+    for i, c in enumerate(cases):
+        c.check(want[i])
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+@pytest.mark.parametrize("lens,max_new", [([(40, 300), (9, 77)], 40), ([(1, 300), (2, 77)], 1)])
+@pytest.mark.parametrize("dim,page", [(8, 16), (128, 7), (64, 1), (256, 5), (64, 16)])
+def test_nothing_of_the_last_call_remains(cuda_dev, lens, max_new, dim, page):
+    """After a call whose values are infinite, which shared memory may still
+    hold, the limits of a call's tiles are cleaned of its own values only."""
+    bad = Case(lens, 8, 2, dim, page, seed=3)
+    for v in bad.values:
+        v.fill_(math.inf)
+    bad.write()
+    c = Case(lens, 8, 2, dim, page, seed=4)
+    first, lse = run(c, max_new)
+    c.check(first, lse)
+    for _ in range(30):
+        qmoe.attn_paged(bad.cache, bad.batch(max_new), bad.q)
+        out, _ = run(c, max_new)
+        assert torch.equal(out, first)
