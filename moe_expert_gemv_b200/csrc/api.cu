@@ -29,6 +29,9 @@ struct DevState {
 
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
+// Held over a call's launches: two threads that share a stream and a workspace
+// must not put one call's second kernel behind the other's first.
+std::mutex g_launch_mu;
 std::atomic<int32_t> g_pdl_enabled{1};
 std::atomic<int32_t> g_prefill_tc_min{0};
 std::atomic<unsigned long long> g_decode_wait_ns{kWaitLimitNs};
@@ -1017,6 +1020,7 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     a.ctr = static_cast<int *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAttnCounterBytes);
     a.status = status_dev ? status_dev : d->status;
+    std::lock_guard<std::mutex> lock(g_launch_mu);
     return cuda_status(launch_attn(a, cache->dtype == QMOE_BF16, max_rows, launch_cfg(d, stream)));
 }
 
@@ -1088,6 +1092,7 @@ qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, in
     a.mask = rules->mask;
     a.mask_stride = rules->mask_stride;
     a.status = status_dev ? status_dev : d->status;
+    std::lock_guard<std::mutex> lock(g_launch_mu);
     return cuda_status(launch_logits(a, dtype, workspace, launch_cfg(d, stream)));
 }
 
