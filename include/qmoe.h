@@ -593,6 +593,8 @@ qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
  * row does not see do not reach it, infinities and NaNs included.
  * q, out: [tokens][heads][head_dim] by strides, 16-byte aligned, strides
  * multiples of 8, the cache's type; lse: fp32 [tokens][heads] or NULL.
+ * scale and softcap finite, scale > 0; a softcap far above the scores leaves
+ * them as they are.
  * Scores, softmax statistics and sums are fp32; a weight enters the second
  * product rounded to the cache's type, the output is rounded once.
  * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device

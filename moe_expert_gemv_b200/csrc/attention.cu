@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
     }
 
     // ==================================================== 4 warps of products
-    const float sc2 = a.softcap > 0.f ? a.scale * 2.f * kLog2e / a.softcap : a.scale * kLog2e;
-    const float cap = a.softcap * kLog2e;
+    const AttnCap cap(a.scale, a.softcap);
+    const float sc2 = a.scale * kLog2e;
     uint32_t n = 0;       // tiles so far
     bool dead = false;    // a wait gave up (uniform in the warp)
     for (; !w.done(); w.next(a)) {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = jw + 8 * i + (e & 1), r = e >> 1;
-                    float x = a.softcap > 0.f ? capped(s[i][e], sc2, cap) : s[i][e] * sc2;
+                    float x = a.softcap > 0.f ? cap.any(s[i][e]) : s[i][e] * sc2;
                     x = j >= lo[r] && j < hi[r] ? x : -INFINITY;
                     s[i][e] = x;
                     mx[r] = fmaxf(mx[r], x);

@@ -317,6 +317,35 @@ __device__ __noinline__ void at_restore(const AttnArgs &a, const Walk &w, int ro
     at_wait_st();
 }
 
+// A warp's rows of scores in tensor memory, capped by a wide cap.  A call, so
+// that its forms take no registers from the softmax of other calls' scores.
+template <int KT>
+__device__ __noinline__ void at_cap(const AttnArgs &a, uint32_t taddr)
+{
+    const AttnCap cap(a.scale, a.softcap);
+#pragma unroll 1
+    for (int c = 0; c < KT; c += 32) {
+        uint32_t s[32];
+        at_ld32(taddr + c, s);
+        at_wait_ld(s);
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            most = fmaxf(most, fabsf(__uint_as_float(s[i])));
+        if (cap.above(most)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                s[i] = __float_as_uint(cap.any(__uint_as_float(s[i])));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                s[i] = __float_as_uint(cap.low(__uint_as_float(s[i])));
+        }
+        at_st32(taddr + c, s);
+    }
+    at_wait_st();
+}
+
 template <class T, int DP, int NROW>
 __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(const AttnArgs a, const __grid_constant__ AttnMaps maps)
 {
@@ -950,6 +979,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
         uint32_t sc = 0, oc = 0, pv = 0;   // sc: parities, a bit each
         bool dead = false;
         const float sc2 = a.softcap > 0.f ? 1.f : a.scale * kLog2e;
+        const bool wide = AttnCap(a.scale, a.softcap).wide;
         for (; !w.done(); advance()) {
             const int nt = w.tb() - w.ta();
             const int rows = min(M, w.s.n * a.group - w.rt * M);
@@ -973,6 +1003,8 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     at_fence_after();
                     const uint32_t ts = tq + C::s_col + buf * 128;
                     const bool cut = __any_sync(0xffffffffu, l0 > 0 || h0 < KT);
+                    if (wide)
+                        at_cap<KT>(a, ts);
                     uint32_t s[KT];
 #pragma unroll
                     for (int c = 0; c < KT; c += 32)
@@ -981,11 +1013,11 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
 #pragma unroll
                     for (int c = 32; c < KT; c += 32)
                         at_pin(s + c);
-                    if (a.softcap > 0.f) {
-                        const float capc = a.scale * 2.f * kLog2e / a.softcap, cap = a.softcap * kLog2e;
+                    if (a.softcap > 0.f && !wide) {
+                        const AttnCap cap(a.scale, a.softcap);
 #pragma unroll
                         for (int c = 0; c < KT; ++c)
-                            s[c] = __float_as_uint(capped(__uint_as_float(s[c]), capc, cap));
+                            s[c] = __float_as_uint(cap.high(__uint_as_float(s[c])));
                     }
                     if (cut) {
 #pragma unroll

@@ -76,14 +76,55 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
-// cap * tanh(x / cap) from tanh(z) = 1 - 2 / (1 + e^2z): one exponential and
-// one reciprocal, absolute error a few 2^-23 of cap (the hardware's tanh is
-// good to 2^-11 of cap only, which would show in the weights).  c2 = 2 log2(e)
-// / cap; cap_out may carry another factor along.
-__device__ __forceinline__ float capped(float x, float c2, float cap_out)
-{
-    return cap_out * (1.f - __fdividef(2.f, 1.f + exp2_approx(x * c2)));
-}
+// log2(e) cap tanh(scale x / cap) of a product x, t = scale x / cap.
+//   high: tanh(t) = 1 - 2 / (1 + e^2t), one exponential and one reciprocal (the
+//     hardware's tanh is good to 2^-11 only, which would show in the weights).
+//     Off by up to 2^-22 of the cap: near t = 0 the 1 cancels.
+//   low, |t| < 1/2: t P(t^2), P by Chebyshev interpolation of tanh(sqrt w) /
+//     sqrt w in 5 points of [0, 1/4] (off by 1.4e-8; 1.1e-7 with its roundings):
+//     a cap that is large beside the scores leaves them as they are.
+// attn_rows_kernel takes both for every score and chooses (64 sequences of up to
+// 4096 tokens: 110.4 us instead of 108.8 with high alone; a branch around them
+// cost calls without a cap 131 instead of 93).  attn_tc_kernel, whose
+// exponentials count, takes high alone up to a cap of 64 -- 2^-16 of a score at
+// most, far below a 16-bit weight's half step -- and above it each score by its
+// t, a warp none of whose scores is high the polynomial alone (at_cap; 8 drafts of
+// 24 with heads of 256: 38.6 us, 35.9 by high alone).
+struct AttnCap {
+    float k, to_t, to_e, cap;   // scale log2 e, scale / cap, 2 log2 e scale / cap, cap log2 e
+    bool wide;
+
+    // (a tiny cap makes t infinite, but for a score of 0, whose t stays 0)
+    __device__ __forceinline__ AttnCap(float scale, float softcap)
+        : k(scale * kLog2e), to_t(fminf(scale / softcap, 1e37f)), to_e(to_t * 2.f * kLog2e), cap(softcap * kLog2e),
+          wide(softcap > 64.f)
+    {
+    }
+    __device__ __forceinline__ float high(float x) const
+    {
+        return cap * (1.f - __fdividef(2.f, 1.f + exp2_approx(x * to_e)));
+    }
+    __device__ __forceinline__ float low(float x) const
+    {
+        const float t = x * to_t, w = t * t;
+        float p = fmaf(w, 0.01713134f, -0.05298424f);
+        p = fmaf(p, w, 0.13324751f);
+        p = fmaf(p, w, -0.33333068f);
+        p = fmaf(p, w, 1.f);
+        return x * k * p;
+    }
+    __device__ __forceinline__ float any(float x) const
+    {
+        const float h = high(x);
+        return fabsf(x * to_t) < 0.5f ? low(x) : h;
+    }
+    // whether a thread of the warp has a score that is not for low(); most: the
+    // thread's largest |x| (NaN stays NaN in both)
+    __device__ __forceinline__ bool above(float most) const
+    {
+        return __any_sync(0xffffffffu, !(most * to_t < 0.5f));
+    }
+};
 
 // ------------------------------------------------------------------- units --
 struct AttnSeq {
