@@ -596,7 +596,9 @@ qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
  * scale and softcap finite, scale > 0; a softcap far above the scores leaves
  * them as they are.
  * Scores, softmax statistics and sums are fp32; a weight enters the second
- * product rounded to the cache's type, the output is rounded once.
+ * product rounded to the cache's type (in fp16, whose smallest step is 2^-24,
+ * relative to 2^7 of the row's largest: one below 2^-32 of the largest counts in
+ * the sum only), the output is rounded once.
  * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device
  * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every
  * call leaves them zero again (but for one that raised QMOE_DEV_TIMEOUT: zero

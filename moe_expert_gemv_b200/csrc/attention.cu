@@ -339,10 +339,10 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) - Num16<T>::kLift;
             }
             // the sums are rescaled only when a maximum has grown by more than 2^8:
-            // until then the weights are at most 2^8, of the same base
+            // until then the weights are at most 2^(8 + kLift), of the same base
             const bool grow = mx[0] > m[0] + AM_LAZY || mx[1] > m[1] + AM_LAZY ||
                               (m[0] == -INFINITY && mx[0] > m[0]) || (m[1] == -INFINITY && mx[1] > m[1]);
             if (__any_sync(0xffffffffu, grow)) {

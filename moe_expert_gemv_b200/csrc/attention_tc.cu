@@ -17,8 +17,8 @@
 // products run.  NROW = 1 (128 rows; head_dim 256, or few rows): the scores
 // of the next key tile are made while the softmax works on this one.
 // O is rescaled only when a row's maximum has grown by more than 2^8 since
-// the last time: until then the weights are at most 2^8 (exact powers of the
-// same base, no rounding is lost), so most tiles touch O in the product only.
+// the last time: until then the weights are at most 2^8 more (exact powers of
+// the same base, no rounding is lost), so most tiles touch O in the product only.
 //
 // Roles: the softmax warpgroups; a warp that issues the products; a TMA warp
 // each for K, V and Q; and a warpgroup that cleans values at the limits and
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     for (int c = 0; c < KT; c += 2)
                         mx[(c >> 1) & 3] =
                             fmaxf(fmaxf(mx[(c >> 1) & 3], __uint_as_float(s[c])), __uint_as_float(s[c + 1]));
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc2;
+                    const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), sc2, -Num16<T>::kLift);
                     if (__any_sync(0xffffffffu, top > m + TC_LAZY || (m == -INFINITY && top > m))) {
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.f : exp2_approx(m - mn);

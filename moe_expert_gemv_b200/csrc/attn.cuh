@@ -41,6 +41,9 @@ struct Num16<__half> {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
     }
     static constexpr uint32_t kExp = 0x7C007C00u;   // exponent bits of a pair
+    // log2 of a row's largest weight as its maximum is set: with the 2^8 that the
+    // maximum may lag behind, at most 2^15, and 2^-32 of it is the smallest step
+    static constexpr float kLift = 7.f;
 };
 template <>
 struct Num16<__nv_bfloat16> {
@@ -59,6 +62,7 @@ struct Num16<__nv_bfloat16> {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
     }
     static constexpr uint32_t kExp = 0x7F807F80u;
+    static constexpr float kLift = 0.f;   // its exponents are fp32's
 };
 
 // whether one of the two 16-bit numbers of a word is an infinity or a NaN

@@ -66,3 +66,28 @@ def test_caps_of_any_size(cuda_dev, lens, heads, kv_heads, new, dim, page, cap):
     out = qmoe.attn_paged(c.cache, c.batch(new), c.q, softcap=cap)
     assert qmoe.qmoe_check_status() == 0
     check(c, out, scale, cap, 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 7), (256, 32)])
+@pytest.mark.parametrize("lens,heads,kv_heads,new", [([(1, 8192), (1, 4097)], 8, 2, 1), ([(20, 8192), (24, 5000)], 8, 2, 24),
+                                                     ([(600, 4300), (600, 700)], 64, 8, 600)], ids=["decode", "drafts", "chunks"])
+def test_many_small_weights(cuda_dev, lens, heads, kv_heads, new, dim, page, dtype):
+    """64 keys of every 4096 have a score of 25.2 log 2 and the value 0, the others
+    score 0 and have the value 1000: their weights, 2^-25.2 of the largest, are
+    all of the output, and a weight that is lost is seen.  At most 2^-32 of the
+    largest each is: half the smallest fp16 step over the 2^7 that the largest
+    is lifted to (it may be up to 2^8 larger, which only helps)."""
+    c = Case(lens, heads, kv_heads, dim, page, dtype, seed=1)
+    c.q.zero_()
+    c.q[..., 0] = 16.0
+    for k, v in zip(c.keys, c.values):
+        k.zero_()
+        v.fill_(1000.0)
+        far = torch.arange(k.shape[0], device="cuda") % 4096 < 64
+        k[far, :, 0] = 25.2 * math.log(2) / 16
+        v[far] = 0.0
+    c.write()
+    out = qmoe.attn_paged(c.cache, c.batch(new), c.q, scale=1.0)
+    assert qmoe.qmoe_check_status() == 0
+    check(c, out, 1.0, 0.0, 2.0 ** -32 if dtype == F16 else 0.0)
