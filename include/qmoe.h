@@ -601,11 +601,10 @@ qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
  * the sum only), the output is rounded once.
  * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device
  * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every
- * call leaves them zero again (but for one that raised QMOE_DEV_TIMEOUT: zero
- * them then), so calls of any shape share it in turn, but not two that can run
- * at the same time.  max_rows: the most rows of one
- * sequence per K/V head in any call, max_new * heads / kv_heads (max_new 0:
- * take `tokens`).
+ * call leaves them zero again (one that raises QMOE_DEV_TIMEOUT too, whose
+ * outputs are invalid), so calls of any shape share it in turn, but not two that
+ * can run at the same time.  max_rows: the most rows of one sequence per K/V
+ * head in any call, max_new * heads / kv_heads (max_new 0: take `tokens`).
  * UNSUPPORTED: head_dim not a multiple of 8 or above 256; tokens * heads / kv_heads
  * above 2^30. */
 typedef struct qmoe_attn {
@@ -700,6 +699,9 @@ int32_t qmoe_set_dependent_launch(int32_t enable);
  * return), in nanoseconds; 0 restores the default of 2 s.  Applies to later
  * calls in this process; returns the previous setting. */
 uint64_t qmoe_set_decode_wait_limit_ns(uint64_t ns);
+
+/* The same for the waits inside attn_paged; below 100000 a wait is one look. */
+uint64_t qmoe_set_attn_wait_limit_ns(uint64_t ns);
 
 /* Experts of a prefill chunk (and the shared expert) with at least
  * `min_tokens` tokens run on the tensor-core (tcgen05) kernels, the others on

@@ -35,6 +35,7 @@ std::mutex g_launch_mu;
 std::atomic<int32_t> g_pdl_enabled{1};
 std::atomic<int32_t> g_prefill_tc_min{0};
 std::atomic<unsigned long long> g_decode_wait_ns{kWaitLimitNs};
+std::atomic<unsigned long long> g_attn_wait_ns{kWaitLimitNs};
 
 qmoe_status device_state(DevState **out)
 {
@@ -1019,6 +1020,8 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     a.causal = attn->causal != 0;
     a.ctr = static_cast<int *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAttnCounterBytes);
+    a.wait_ns = g_attn_wait_ns.load();
+    a.wait_ns = a.wait_ns < kSuspendHintNs ? 0 : a.wait_ns;   // what a look may be parked for
     a.status = status_dev ? status_dev : d->status;
     std::lock_guard<std::mutex> lock(g_launch_mu);
     return cuda_status(launch_attn(a, cache->dtype == QMOE_BF16, max_rows, launch_cfg(d, stream)));
@@ -1176,6 +1179,11 @@ int32_t qmoe_set_dependent_launch(int32_t enable)
 uint64_t qmoe_set_decode_wait_limit_ns(uint64_t ns)
 {
     return g_decode_wait_ns.exchange(ns == 0 ? kWaitLimitNs : ns);
+}
+
+uint64_t qmoe_set_attn_wait_limit_ns(uint64_t ns)
+{
+    return g_attn_wait_ns.exchange(ns == 0 ? kWaitLimitNs : ns);
 }
 
 int32_t qmoe_set_prefill_tensor_min(int32_t min_tokens)

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
                 if (t + 1 < tb && bx < nbox)   // on its way while this tile's copies go out
                     ahead = attn_page(a, w.sp.b, j + AM_KT, w.lo, w.hi);
                 if (n >= S &&
-                    !__all_sync(0xffffffffu, at_wait(&empty[n % S], (n / S - 1) & 1, a.status, abort_word))) {
+                    !__all_sync(0xffffffffu, at_wait(&empty[n % S], (n / S - 1) & 1, a, abort_word))) {
                     dead = true;
                     break;
                 }
@@ -172,7 +172,10 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
     const AttnCap cap(a.scale, a.softcap);
     const float sc2 = a.scale * kLog2e;
     uint32_t n = 0;       // tiles so far
-    bool dead = false;    // a wait gave up (uniform in the warp)
+    // A wait gave up in this warp; after its unit, in any of the CTA's.  The tiles
+    // are passed over then (the outputs are flagged as invalid), and the CTA
+    // arrives as ever, so that the counters of shared units come to zero.
+    bool dead = false;
     for (; !w.done(); w.next(a)) {
         const int ta = w.ta(), tb = w.tb();
         const int row0 = w.rt * M;
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
             long long noff = -1;
             const int st = TMA ? n % S : t % S;
             if (TMA) {
-                dead = dead || !__all_sync(0xffffffffu, at_wait(&full[st], (n / S) & 1, a.status, abort_word));
+                dead = dead || !__all_sync(0xffffffffu, at_wait(&full[st], (n / S) & 1, a, abort_word));
             } else {
                 cp_async_wait<S - 2>();
                 named_bar_sync(1, AM_THREADS);
@@ -401,8 +404,7 @@ __global__ void __launch_bounds__(AM_THREADS + (TMA ? 32 : 0))
             if (tg == 0)
                 ml[warp * M + g + 8 * r] = make_float2(m[r], l[r]);
         }
-        if (bar_any(1, AM_THREADS, dead))
-            break;
+        dead = bar_any(1, AM_THREADS, dead);
         for (int k = 0; k < 4; ++k) {
             if (warp == k) {
 #pragma unroll
@@ -500,6 +502,8 @@ cudaError_t launch_rows(const AttnArgs &a, const AttnMaps &maps, const LaunchCfg
     cudaError_t e = set_smem(kern, L::total);
     if (e != cudaSuccess)
         return e;
+    // (and up to 168 registers a thread: 224 once took 131 us where 165 take 93; a
+    // bound of two blocks in the declaration spills 24 bytes and takes 94)
     constexpr int per_sm = DP == 256 ? 1 : 2;
     static_assert(per_sm * (L::total + 1024) <= 228 * 1024 && per_sm <= 3, "shared memory");
     return launch_ex(kern, dim3(c.num_sms * per_sm), dim3(AM_THREADS + (TMA ? 32 : 0)), L::total, c, 1, a, maps);

@@ -231,7 +231,7 @@ __device__ __forceinline__ void at_scale16(uint32_t taddr, float f)
 }
 
 // bounded wait until a stage has been armed for tile `n`
-__device__ __forceinline__ bool at_armed(volatile int *arm, int n, int32_t *status, volatile int *abort_word)
+__device__ __forceinline__ bool at_armed(volatile int *arm, int n, const AttnArgs &a, volatile int *abort_word)
 {
     if (*arm == n)
         return true;
@@ -240,8 +240,8 @@ __device__ __forceinline__ bool at_armed(volatile int *arm, int n, int32_t *stat
         __nanosleep(20);
         if (*abort_word)
             return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            flag_status(status, QMOE_DEV_TIMEOUT);
+        if (global_timer_ns() - t0 >= a.wait_ns) {
+            flag_status(a.status, QMOE_DEV_TIMEOUT);
             *abort_word = 1;
             return false;
         }
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
             uint32_t pc = 0, oc = 0, xc = 0, given = 0;
             bool ok = true, issued = false;
             auto wait = [&](int b, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, at_wait(&bar[b], parity & 1, a.status, abort_word));
+                ok = ok && __all_sync(0xffffffffu, at_wait(&bar[b], parity & 1, a, abort_word));
                 return ok;
             };
             auto commit = [&](int b) {
@@ -650,8 +650,8 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     d->c1 = w.c1();
                 }
                 for (int rt = 0; rt < NROW && rt * 128 < rows; ++rt) {
-                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_LF + rt], (oc >> rt) & 1, a.status, abort_word) &&
-                                                     at_wait(&bar[TB_OF + rt], (oc >> rt) & 1, a.status, abort_word))) {
+                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_LF + rt], (oc >> rt) & 1, a, abort_word) &&
+                                                     at_wait(&bar[TB_OF + rt], (oc >> rt) & 1, a, abort_word))) {
                         dead = true;
                         return;
                     }
@@ -754,7 +754,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         if (t + 1 < tb && lane < nbox)   // on its way while this tile's copies go out
                             ahead = attn_page(a, w.sp.b, j + KT, w.lo, w.hi);
                         if (n >= 2 && !__all_sync(0xffffffffu, at_wait(&bar[(x ? TB_VE : TB_KE) + n % 2], (n / 2 - 1) & 1,
-                                                                       a.status, abort_word))) {
+                                                                       a, abort_word))) {
                             dead = true;
                             break;
                         }
@@ -787,7 +787,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
                         const int nr = NROW == 2 && rows > 128 ? 2 : 1;
                         if (un > 0 && !__all_sync(0xffffffffu,
-                                                  at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))) {
+                                                  at_wait(&bar[TB_QE], (un - 1) & 1, a, abort_word))) {
                             dead = true;
                             break;
                         }
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     const int row0 = w.rt * M, rows = min(M, w.s.n * a.group - row0);
                     // (with Q on TMA these warps must not wait for it: its next use may
                     // be over before they come here)
-                    if (un > 0 && !a.tma_q && !at_wait(&bar[TB_QE], (un - 1) & 1, a.status, abort_word))
+                    if (un > 0 && !a.tma_q && !at_wait(&bar[TB_QE], (un - 1) & 1, a, abort_word))
                         dead = true;
                     if (bar_any(TC_BAR_LOAD, C::LOAD, dead))
                         break;
@@ -840,8 +840,8 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         const uint32_t s = n + (i - ta);
                         // armed first: a parity tells two uses of a stage apart only
                         // once the earlier one is over
-                        if (!at_armed(&armed_v[s % 2], (int)s, a.status, abort_word) ||
-                            !at_wait(&bar[TB_VF + s % 2], (s / 2) & 1, a.status, abort_word)) {
+                        if (!at_armed(&armed_v[s % 2], (int)s, a, abort_word) ||
+                            !at_wait(&bar[TB_VF + s % 2], (s / 2) & 1, a, abort_word)) {
                             dead = true;
                             break;
                         }
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                     if (mbar_try_wait_now(&bar[b], parity))
                         return;
                     flush();
-                    if (!at_wait(&bar[b], parity, a.status, abort_word))
+                    if (!at_wait(&bar[b], parity, a, abort_word))
                         dead = true;
                 };
                 auto slot = [&](int t, int tb, int r) {
@@ -995,7 +995,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 }
                 for (int t = 0; t < nt; ++t, l0 -= KT, h0 -= KT) {
                     const int buf = NROW == 2 ? rt : t & 1;
-                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_SF + buf], (sc >> buf) & 1, a.status, abort_word))) {
+                    if (!__all_sync(0xffffffffu, at_wait(&bar[TB_SF + buf], (sc >> buf) & 1, a, abort_word))) {
                         dead = true;
                         break;
                     }
@@ -1045,7 +1045,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                         if (t > 0) {
                             // O holds the products up to the last tile's
                             if (NROW == 1 &&
-                                !__all_sync(0xffffffffu, at_wait(&bar[TB_PV], (pv - 1) & 1, a.status, abort_word))) {
+                                !__all_sync(0xffffffffu, at_wait(&bar[TB_PV], (pv - 1) & 1, a, abort_word))) {
                                 dead = true;
                                 break;
                             }
@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(TcCfg<DP, NROW>::THREADS, 1) attn_tc_kernel(co
                 // the row's maximum and sum for the output, once the last unit's have
                 // been read (before its O was given back)
                 if (!dead && oc > 0 &&
-                    !__all_sync(0xffffffffu, at_wait(&bar[TB_OE + rt], (oc - 1) & 1, a.status, abort_word)))
+                    !__all_sync(0xffffffffu, at_wait(&bar[TB_OE + rt], (oc - 1) & 1, a, abort_word)))
                     dead = true;
                 if (!dead) {
                     ++oc;

@@ -12,7 +12,8 @@
 // graph replays with new ones).  Each unit is EX places longer on the line
 // than its tiles: what it costs to begin and end one, in tiles.  A unit that crosses CTA borders is finished
 // by its last CTA to arrive, which adds the fp32 partial results in tile
-// order; nobody waits, and results do not depend on the order of arrival.
+// order; nobody waits, and results do not depend on the order of arrival.  A CTA
+// that gives up a wait arrives all the same, so that the counters end at zero.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -346,26 +347,6 @@ __device__ __forceinline__ long long attn_slot(const AttnArgs &a, int b, int h, 
     return id * a.page_stride + (long long)(j - pg * a.page_size) * a.token_stride + h * a.head_stride;
 }
 
-// bounded wait that gives up at once after another thread of the CTA did
-__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, int32_t *status, volatile int *abort_word)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    if (*abort_word)
-        return false;
-    if (mbar_wait(bar, parity, status))
-        return true;
-    *abort_word = 1;
-    return false;
-}
-
-// byte offset of 16-byte unit c of row r in a tile of `rows` rows, in 128-byte
-// swizzled blocks of 64 columns
-__device__ __forceinline__ uint32_t at_sw(int rows, int r, int c)
-{
-    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // one look at a barrier, without being parked
 __device__ __forceinline__ bool mbar_try_wait_now(uint64_t *bar, uint32_t parity)
 {
@@ -378,6 +359,32 @@ __device__ __forceinline__ bool mbar_try_wait_now(uint64_t *bar, uint32_t parity
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// Wait of at most a.wait_ns (flags QMOE_DEV_TIMEOUT; 0: one look) that gives up
+// at once after another thread of the CTA did.  Copies and products in flight are
+// awaited by mbar_wait, whose limit is not the caller's.
+__device__ __forceinline__ bool at_wait(uint64_t *bar, uint32_t parity, const AttnArgs &a, volatile int *abort_word)
+{
+    if (mbar_try_wait_now(bar, parity))
+        return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (!*abort_word) {
+        if (global_timer_ns() - t0 >= a.wait_ns) {
+            flag_status(a.status, QMOE_DEV_TIMEOUT);
+            *abort_word = 1;
+        } else if (mbar_try_wait(bar, parity)) {
+            return true;
+        }
+    }
+    return false;
+}
+
+// byte offset of 16-byte unit c of row r in a tile of `rows` rows, in 128-byte
+// swizzled blocks of 64 columns
+__device__ __forceinline__ uint32_t at_sw(int rows, int r, int c)
+{
+    return (uint32_t)((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live)

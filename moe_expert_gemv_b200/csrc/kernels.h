@@ -272,6 +272,7 @@ struct AttnArgs {
     int heads_inner;                 // order of the map's middle dimensions: heads, then slots
     float *part;                     // partial results of units that several CTAs share
     int *ctr;                        // their arrival counters, zero between calls
+    unsigned long long wait_ns;      // limit of a wait, 0: one look at it
     int32_t *status;
 };
 // rows (tokens x query heads of one K/V head) of the longest sequence decide

@@ -99,6 +99,7 @@ def lib():
             "qmoe_set_dependent_launch": [i32],
             "qmoe_set_prefill_tensor_min": [i32],
             "qmoe_set_decode_wait_limit_ns": [ctypes.c_uint64],
+            "qmoe_set_attn_wait_limit_ns": [ctypes.c_uint64],
             "qmoe_version": [],
             "qmoe_lfu_create": [i32, p],
             "qmoe_lfu_destroy": [p],
@@ -126,6 +127,7 @@ def lib():
         L.qmoe_set_dependent_launch.restype = i32
         L.qmoe_set_prefill_tensor_min.restype = i32
         L.qmoe_set_decode_wait_limit_ns.restype = ctypes.c_uint64
+        L.qmoe_set_attn_wait_limit_ns.restype = ctypes.c_uint64
         L.qmoe_lfu_destroy.restype = None
         L.qmoe_cache_destroy.restype = None
         L.qmoe_lfu_plan.restype = i32
@@ -1091,6 +1093,12 @@ def qmoe_set_decode_wait_limit_ns(ns):
     """Limit of every wait inside the fused decode (0: the default 2 s).
     Returns the previous setting."""
     return int(lib().qmoe_set_decode_wait_limit_ns(int(ns)))
+
+
+def qmoe_set_attn_wait_limit_ns(ns):
+    """Limit of every wait inside attn_paged (0: the default 2 s).  Returns the
+    previous setting."""
+    return int(lib().qmoe_set_attn_wait_limit_ns(int(ns)))
 
 
 # the threshold used when the tensor-core prefill path is switched on (the
