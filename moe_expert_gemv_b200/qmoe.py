@@ -711,6 +711,7 @@ def _packer(cls):
 
 
 _pack_rows, _pack_attn, _pack_rules = _packer(CRows), _packer(CAttn), _packer(CLogitRules)
+_pack_batch = _packer(CKVBatch)
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
@@ -777,7 +778,8 @@ def _rows(t, what, dtype, device, shape):
 class KVCache:
     """One layer's paged K/V cache: k, v float16 or bfloat16 [num_pages]
     [page_size][kv_heads][head_dim], both with the same strides (a transposed
-    view of [num_pages][kv_heads][page_size][head_dim] tensors is as good)."""
+    view of [num_pages][kv_heads][page_size][head_dim] tensors is as good).
+    Other tensors are another cache: k and v cannot be replaced."""
 
     def __init__(self, k, v):
         for t, what in ((k, "k"), (v, "v")):
@@ -789,11 +791,14 @@ class KVCache:
             raise ValueError("k and v must agree in type, shape, strides and device")
         if k.stride(3) != 1:
             raise ValueError("the elements of a head must follow each other")
-        self.k, self.v, self.device, self.dtype = k, v, k.device, k.dtype
+        self._k, self._v, self.device, self.dtype = k, v, k.device, k.dtype
         self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         strides = [k.stride(i) if k.shape[i] > 1 else 0 for i in range(3)]
         self.c = CKVCache(k.data_ptr(), v.data_ptr(), *strides, *k.shape, _DTYPES[k.dtype])
         self._ref = ctypes.addressof(self.c)
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
 
     @classmethod
     def empty(cls, num_pages, page_size, kv_heads, head_dim, dtype=torch.float16, device="cuda"):
@@ -805,29 +810,65 @@ class KVBatch:
     """A step's sequences: page_table int32 [B][max_pages], q_start int32
     [B + 1] (sequence b's new tokens are rows q_start[b] .. q_start[b+1]),
     kv_len int32 [B] (cached tokens with the new ones).  max_new: an upper
-    bound of the new tokens per sequence, which chooses the kernel."""
+    bound of the new tokens per sequence, which chooses the kernel.  Each can
+    be replaced between calls by another of the same batch and device."""
 
     def __init__(self, page_table, q_start, kv_len, max_new=0):
         _need(page_table, torch.int32, "page_table")
         if page_table.dim() != 2 or page_table.numel() == 0:
             raise ValueError("page_table must be [batch][pages], not empty")
-        B = page_table.shape[0]
-        _need(q_start, torch.int32, "q_start", (B + 1,))
-        _need(kv_len, torch.int32, "kv_len", (B,))
-        self.device = page_table.device
-        _on(self.device, q_start, "q_start")
-        _on(self.device, kv_len, "kv_len")
-        self.page_table, self.q_start, self.kv_len, self.max_new = page_table, q_start, kv_len, int(max_new)
-        self._by_tokens = {}
+        self.device, self._batch = page_table.device, page_table.shape[0]
+        self._held = None   # (tokens, the C struct for steps of so many rows)
+        self._page_table, self.q_start, self.kv_len, self.max_new = page_table, q_start, kv_len, max_new
+
+    def _lens(self, t, what, n):
+        _need(t, torch.int32, what, (n,))
+        self._held = None
+        return _on(self.device, t, what)
+
+    @property
+    def page_table(self):
+        return self._page_table
+
+    @page_table.setter
+    def page_table(self, t):
+        _need(t, torch.int32, "page_table")
+        if t.dim() != 2 or t.shape[0] != self._batch or t.shape[1] == 0:
+            raise ValueError("page_table must be [%d][pages]" % self._batch)
+        self._page_table, self._held = _on(self.device, t, "page_table"), None
+
+    @property
+    def q_start(self):
+        return self._q_start
+
+    @q_start.setter
+    def q_start(self, t):
+        self._q_start = self._lens(t, "q_start", self._batch + 1)
+
+    @property
+    def kv_len(self):
+        return self._kv_len
+
+    @kv_len.setter
+    def kv_len(self, t):
+        self._kv_len = self._lens(t, "kv_len", self._batch)
+
+    @property
+    def max_new(self):
+        return self._max_new
+
+    @max_new.setter
+    def max_new(self, n):
+        self._max_new, self._held = int(n), None
 
     def _c(self, tokens):
-        """Address of the C struct for steps of `tokens` rows."""
-        held = self._by_tokens.get(tokens)
-        if held is None:
-            c = CKVBatch(self.page_table.data_ptr(), self.q_start.data_ptr(), self.kv_len.data_ptr(),
-                         self.page_table.shape[0], self.page_table.shape[1], tokens, self.max_new)
-            held = self._by_tokens[tokens] = (ctypes.addressof(c), c)
-        return held[0]
+        """The C struct for steps of `tokens` rows, and its max_new."""
+        held = self._held
+        if held is None or held[0] != tokens:
+            held = self._held = (tokens, _pack_batch(
+                self._page_table.data_ptr(), self._q_start.data_ptr(), self._kv_len.data_ptr(), self._batch,
+                self._page_table.shape[1], tokens, self._max_new), self._max_new)
+        return held[1:]
 
 
 def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, trained=0, low=1.0, high=4.0):
@@ -841,15 +882,18 @@ def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, trained=0,
 
 class Rope:
     """Rotary positions: inv_freq float64 [rot_dim / 2] on the GPU, layout
-    "half" or "interleaved", scale of the turned part."""
+    "half" or "interleaved", scale of the turned part.  Another table is another
+    Rope: inv_freq cannot be replaced."""
 
     def __init__(self, inv_freq, layout="half", scale=1.0):
         _need(inv_freq, torch.float64, "inv_freq")
         if inv_freq.dim() != 1 or inv_freq.numel() == 0:
             raise ValueError("inv_freq must be [rot_dim / 2]")
-        self.inv_freq, self.device, self.rot_dim = inv_freq, inv_freq.device, 2 * inv_freq.numel()
+        self._inv_freq, self.device, self.rot_dim = inv_freq, inv_freq.device, 2 * inv_freq.numel()
         self.c = CRope(inv_freq.data_ptr(), self.rot_dim, ROPE_LAYOUTS[layout], scale)
         self._ref = ctypes.addressof(self.c)
+
+    inv_freq = property(lambda self: self._inv_freq)
 
     @classmethod
     def make(cls, rot_dim, layout="half", device="cuda", **kw):
@@ -900,7 +944,7 @@ def kv_append(cache, batch, k, v, q=None, rope=None, positions=None, q_out=None,
         co = _pack_rows(*_rows(q_out, "q_out", dt, dev, shape))
     if T == 0:   # empty tensors have no address
         return q_out
-    _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T), rope._ref if rope else None,
+    _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T)[0], rope._ref if rope else None,
                  _opt(positions, torch.int32, "positions", (T,), dev), cq, co, heads, ck, cv, _status(status, dev))
     return q_out
 
@@ -962,13 +1006,14 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
         lse = torch.empty(T, H, dtype=torch.float32, device=dev)
     if T == 0:   # empty tensors have no address
         return out if lse is None else (out, lse)
+    cb, max_new = batch._c(T)
     if workspace is None:
-        workspace = _attn_workspace(D, max((batch.max_new or T) * (H // cache.kv_heads), 1), dev)
+        workspace = _attn_workspace(D, max((max_new or T) * (H // cache.kv_heads), 1), dev)
     else:
         _on(dev, workspace, "workspace")
     c = _pack_attn(q_ptr, q_token, q_head, o_ptr, o_token, o_head, _opt(lse, torch.float32, "lse", (T, H), dev), H,
                    window, 1 if causal else 0, D ** -0.5 if scale is None else scale, softcap)
-    _device_call(lib().attn_paged, "attn_paged", dev, c, cache._ref, batch._c(T), workspace.data_ptr(),
+    _device_call(lib().attn_paged, "attn_paged", dev, c, cache._ref, cb, workspace.data_ptr(),
                  workspace.numel() * workspace.element_size(), _status(status, dev))
     return out if lse is None else (out, lse)
 
