@@ -964,7 +964,9 @@ def attn_workspace(head_dim, max_rows, device="cuda"):
     return ws
 
 
-_attn_need = {}
+@functools.lru_cache(maxsize=64)
+def _attn_need(head_dim, max_rows):
+    return lib().attn_paged_workspace_bytes(head_dim, max_rows)
 
 
 def _attn_workspace(head_dim, max_rows, device):
@@ -972,12 +974,9 @@ def _attn_workspace(head_dim, max_rows, device):
     zeros are set by the graph)."""
     if torch.cuda.is_current_stream_capturing():
         return attn_workspace(head_dim, max_rows, device)
-    need = _attn_need.get((head_dim, max_rows))
-    if need is None:
-        need = _attn_need[head_dim, max_rows] = lib().attn_paged_workspace_bytes(head_dim, max_rows)
     key = (device.index, _raw_stream(device))
     ws = _attn_ws.get(key)
-    if ws is None or ws.numel() < need:
+    if ws is None or ws.numel() < _attn_need(head_dim, max_rows):
         ws = _attn_ws[key] = attn_workspace(head_dim, max_rows, device)
     return ws
 
@@ -1022,7 +1021,7 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
 _logits_ws = {}   # one workspace for each device and stream
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=64)   # a history that grows is another width at every step
 def _logits_need(rows, max_history):
     return lib().logits_process_workspace_bytes(rows, max_history)
 
@@ -1092,8 +1091,10 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
         key = (dev.index, _raw_stream(dev))
         held = None if torch.cuda.is_current_stream_capturing() else _logits_ws.get(key)
         if held is None or held.numel() < need:
-            held = torch.empty(need, dtype=torch.uint8, device=dev)
-            if not torch.cuda.is_current_stream_capturing():   # a capture's stays with its graph
+            capturing = torch.cuda.is_current_stream_capturing()   # a capture's stays with its graph
+            # room for a history that grows by a quarter
+            held = torch.empty(need if capturing else need + need // 4, dtype=torch.uint8, device=dev)
+            if not capturing:
                 _logits_ws[key] = held
         ws, nbytes = held.data_ptr(), held.numel()
     _device_call(lib().logits_process, "logits_process", dev, c, logits.data_ptr(), in_stride if R > 1 else V,

@@ -79,3 +79,23 @@ def test_refused_replacements(cuda_dev):
         with pytest.raises(AttributeError):
             setattr(h, name, torch.empty_like(getattr(h, name)))
     c.check(qmoe.attn_paged(c.cache, b, c.q))
+
+
+def test_a_history_that_grows(cuda_dev):
+    """What the binding keeps between calls stays as small as it is, and a
+    stream's workspace is not made anew for every token."""
+    x = torch.zeros(2, 300, device="cuda")
+    hist = torch.zeros(2, 3000, dtype=torch.int32, device="cuda")
+    n = torch.full((2,), 3000, dtype=torch.int32, device="cuda")
+    one = torch.ones(2, device="cuda")
+    stream, seen = torch.cuda.Stream(), set()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for w in range(2500, 2700):
+            y = qmoe.logits_process(x, history=hist[:, :w], history_len=n, presence=one)
+            seen.add(qmoe._logits_ws[x.device.index, stream.cuda_stream].data_ptr())
+            qmoe._attn_need(64, w)
+        assert len(seen) == 1 and (y[:, 0] == -1).all() and not y[:, 1:].any()
+        assert qmoe.qmoe_check_status() == 0
+    for f in (qmoe._logits_need, qmoe._attn_need):
+        assert f.cache_info().maxsize == 64 >= f.cache_info().currsize
