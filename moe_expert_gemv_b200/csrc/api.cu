@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_turn.h"
 
 namespace qmoe {
 
@@ -29,9 +30,6 @@ struct DevState {
 
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
-// Held over a call's launches: two threads that share a stream and a workspace
-// must not put one call's second kernel behind the other's first.
-std::mutex g_launch_mu;
 std::atomic<int32_t> g_pdl_enabled{1};
 std::atomic<int32_t> g_prefill_tc_min{0};
 std::atomic<unsigned long long> g_decode_wait_ns{kWaitLimitNs};
@@ -1023,7 +1021,7 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     a.wait_ns = g_attn_wait_ns.load();
     a.wait_ns = a.wait_ns < kSuspendHintNs ? 0 : a.wait_ns;   // what a look may be parked for
     a.status = status_dev ? status_dev : d->status;
-    std::lock_guard<std::mutex> lock(g_launch_mu);
+    const LaunchTurn turn(workspace);
     return cuda_status(launch_attn(a, cache->dtype == QMOE_BF16, max_rows, launch_cfg(d, stream)));
 }
 
@@ -1095,7 +1093,7 @@ qmoe_status logits_process(const qmoe_logit_rules *rules, const void *logits, in
     a.mask = rules->mask;
     a.mask_stride = rules->mask_stride;
     a.status = status_dev ? status_dev : d->status;
-    std::lock_guard<std::mutex> lock(g_launch_mu);
+    const LaunchTurn turn(need > 0 ? workspace : nullptr);
     return cuda_status(launch_logits(a, dtype, workspace, launch_cfg(d, stream)));
 }
 
