@@ -18,7 +18,7 @@ using qmoe::LaunchTurn;
 
 int main()
 {
-    int a, b;
+    int a = 0, b = 0;
     // while one call launches, those of another workspace and of none do
     LaunchTurn first(&a);
     std::atomic<int> done{0};
