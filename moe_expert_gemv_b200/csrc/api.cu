@@ -1014,7 +1014,9 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
     a.by_page = FastDiv((uint32_t)cache->page_size);
     a.scale = attn->scale;
     a.softcap = attn->softcap;
-    a.window = attn->window;
+    // no position reaches 2^30: a window of as many keys is none, and the first key
+    // of a row before its sequence's beginning stays a 32-bit number
+    a.window = attn->window < (1 << 30) ? attn->window : 0;
     a.causal = attn->causal != 0;
     a.ctr = static_cast<int *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAttnCounterBytes);

@@ -91,3 +91,15 @@ def test_many_small_weights(cuda_dev, lens, heads, kv_heads, new, dim, page, dty
     out = qmoe.attn_paged(c.cache, c.batch(new), c.q, scale=1.0)
     assert qmoe.qmoe_check_status() == 0
     check(c, out, 1.0, 0.0, 2.0 ** -32 if dtype == F16 else 0.0)
+
+
+@pytest.mark.parametrize("window", [1 << 29, (1 << 30) - 1, 1 << 30, (1 << 31) - 1])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("max_new", [1, 40])
+def test_the_widest_windows(cuda_dev, window, causal, max_new):
+    """As no window, also for rows before their sequence's beginning, which see
+    keys where the mask is not causal."""
+    c = Case([(6, 2), (3, 1), (4, 0), (5, 300), (1, 1)], 6, 2, 64, 16)
+    out, lse = qmoe.attn_paged(c.cache, c.batch(max_new), c.q, window=window, causal=causal, want_lse=True)
+    assert qmoe.qmoe_check_status() == 0
+    c.check(out, lse, causal=causal)
