@@ -721,6 +721,14 @@ def _raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _capturing(device):
+    """Whether the current stream of `device`, current or not, is being captured."""
+    if device.index == torch._C._cuda_getDevice():
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.device(device):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _device_call(fn, what, device, *args):
     """fn(*args, current stream of `device`) with `device` current."""
     if device.index == torch._C._cuda_getDevice():
@@ -972,7 +980,7 @@ def _attn_need(head_dim, max_rows):
 def _attn_workspace(head_dim, max_rows, device):
     """One workspace for each stream; in a capture one of the graph's own (its
     zeros are set by the graph)."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(device):
         return attn_workspace(head_dim, max_rows, device)
     key = (device.index, _raw_stream(device))
     ws = _attn_ws.get(key)
@@ -1089,9 +1097,9 @@ def logits_process(logits, out=None, history=None, history_len=None, prompt_len=
         ws, nbytes = _on(dev, workspace, "workspace").data_ptr(), workspace.numel() * workspace.element_size()
     elif need:
         key = (dev.index, _raw_stream(dev))
-        held = None if torch.cuda.is_current_stream_capturing() else _logits_ws.get(key)
+        capturing = _capturing(dev)   # a capture's stays with its graph
+        held = None if capturing else _logits_ws.get(key)
         if held is None or held.numel() < need:
-            capturing = torch.cuda.is_current_stream_capturing()   # a capture's stays with its graph
             # room for a history that grows by a quarter
             held = torch.empty(need if capturing else need + need // 4, dtype=torch.uint8, device=dev)
             if not capturing:
