@@ -870,13 +870,13 @@ class KVBatch:
         self._max_new, self._held = int(n), None
 
     def _c(self, tokens):
-        """The C struct for steps of `tokens` rows, and its max_new."""
+        """(tokens, the C struct for steps of so many rows, its max_new)."""
         held = self._held
         if held is None or held[0] != tokens:
             held = self._held = (tokens, _pack_batch(
                 self._page_table.data_ptr(), self._q_start.data_ptr(), self._kv_len.data_ptr(), self._batch,
                 self._page_table.shape[1], tokens, self._max_new), self._max_new)
-        return held[1:]
+        return held
 
 
 def rope_frequencies(rot_dim, base=10000.0, kind="plain", factor=1.0, trained=0, low=1.0, high=4.0):
@@ -952,7 +952,7 @@ def kv_append(cache, batch, k, v, q=None, rope=None, positions=None, q_out=None,
         co = _pack_rows(*_rows(q_out, "q_out", dt, dev, shape))
     if T == 0:   # empty tensors have no address
         return q_out
-    _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T)[0], rope._ref if rope else None,
+    _device_call(lib().kv_append, "kv_append", dev, cache._ref, batch._c(T)[1], rope._ref if rope else None,
                  _opt(positions, torch.int32, "positions", (T,), dev), cq, co, heads, ck, cv, _status(status, dev))
     return q_out
 
@@ -1013,15 +1013,16 @@ def attn_paged(cache, batch, q, out=None, lse=None, want_lse=False, scale=None, 
         lse = torch.empty(T, H, dtype=torch.float32, device=dev)
     if T == 0:   # empty tensors have no address
         return out if lse is None else (out, lse)
-    cb, max_new = batch._c(T)
+    held = batch._c(T)
     if workspace is None:
-        workspace = _attn_workspace(D, max((max_new or T) * (H // cache.kv_heads), 1), dev)
+        workspace = _attn_workspace(D, max((held[2] or T) * (H // cache.kv_heads), 1), dev)
     else:
         _on(dev, workspace, "workspace")
-    c = _pack_attn(q_ptr, q_token, q_head, o_ptr, o_token, o_head, _opt(lse, torch.float32, "lse", (T, H), dev), H,
-                   window, 1 if causal else 0, D ** -0.5 if scale is None else scale, softcap)
-    _device_call(lib().attn_paged, "attn_paged", dev, c, cache._ref, cb, workspace.data_ptr(),
-                 workspace.numel() * workspace.element_size(), _status(status, dev))
+    c = _pack_attn(q_ptr, q_token, q_head, o_ptr, o_token, o_head,
+                   0 if lse is None else _opt(lse, torch.float32, "lse", (T, H), dev), H, window, 1 if causal else 0,
+                   D ** -0.5 if scale is None else scale, softcap)
+    _device_call(lib().attn_paged, "attn_paged", dev, c, cache._ref, held[1], workspace.data_ptr(),
+                 workspace.numel() * workspace.element_size(), None if status is None else _status(status, dev))
     return out if lse is None else (out, lse)
 
 
