@@ -536,7 +536,7 @@ typedef struct qmoe_kv_batch {
  *                     to whole pairs); *scale = 0.1 ln(factor) + 1
  * and *scale (1 but for RAMP).  trained, low, high are read by the last two
  * only.  INVALID_ARG: rot_dim odd or < 2 (BASE: < 4), base <= 1, factor < 1,
- * trained < 1 or not 0 < low < high. */
+ * trained < 1, not 0 < low < high, or one of them infinite (a raised base too). */
 #define QMOE_ROPE_HALF 0
 #define QMOE_ROPE_INTERLEAVED 1
 #define QMOE_ROPE_PLAIN 0

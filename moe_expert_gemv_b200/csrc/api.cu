@@ -774,15 +774,17 @@ qmoe_status rope_frequencies(int32_t rot_dim, double base, int32_t kind, double 
     if (!inv_freq || !scale || rot_dim < 2 || rot_dim % 2 || !(base > 1.0) || kind < QMOE_ROPE_PLAIN ||
         kind > QMOE_ROPE_RAMP)
         return QMOE_ERR_INVALID_ARG;
-    if (kind != QMOE_ROPE_PLAIN && !(factor >= 1.0))
+    if (kind != QMOE_ROPE_PLAIN && !(factor >= 1.0 && std::isfinite(factor)))
         return QMOE_ERR_INVALID_ARG;
     if (kind == QMOE_ROPE_BASE && rot_dim < 4)
         return QMOE_ERR_INVALID_ARG;
-    if (kind >= QMOE_ROPE_BANDS && (trained < 1 || !(low > 0.0) || !(high > low)))
+    if (kind >= QMOE_ROPE_BANDS && (trained < 1 || !(low > 0.0) || !(high > low) || std::isinf(high)))
         return QMOE_ERR_INVALID_ARG;
     const double two_pi = 6.283185307179586;
     if (kind == QMOE_ROPE_BASE)
         base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+    if (std::isinf(base))   // as given or raised: every frequency but the first would be 0
+        return QMOE_ERR_INVALID_ARG;
     // RAMP: the pair that turns n times over the trained length, trained
     // base^(-2i/R) = 2 pi n, at i = R ln(trained / (2 pi n)) / (2 ln base)
     const int half = rot_dim / 2;
