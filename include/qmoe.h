@@ -598,7 +598,7 @@ qmoe_status kv_append(const qmoe_kv_cache *cache, const qmoe_kv_batch *batch,
  * Scores, softmax statistics and sums are fp32; a weight enters the second
  * product rounded to the cache's type (in fp16, whose smallest step is 2^-24,
  * relative to 2^7 of the row's largest: one below 2^-32 of the largest counts in
- * the sum only), the output is rounded once.
+ * the sum only, and makes NaN of an infinite value), the output is rounded once.
  * workspace: attn_paged_workspace_bytes(head_dim, max rows) bytes of device
  * memory, 16-byte aligned, its first 4096 bytes ZERO before the first use; every
  * call leaves them zero again (one that raises QMOE_DEV_TIMEOUT too, whose
@@ -642,7 +642,7 @@ qmoe_status attn_paged(const qmoe_attn *attn, const qmoe_kv_cache *cache,
  * Ids of -1 are unused places; other ids outside the vocabulary are skipped
  * and raise QMOE_DEV_BAD_TOKEN.  mask: uint32 [rows] of mask_stride words, or
  * mask_stride 0: one mask for all rows.  logits, out: [rows][vocab] by row
- * strides (elements); out may be logits.  rows 0..65535, vocab >= 1.
+ * strides (elements); out may be logits or lies apart from it.  rows 0..65535, vocab >= 1.
  * workspace: logits_process_workspace_bytes(rows, max_history) bytes of device
  * memory, 16-byte aligned, no initial contents required, not used by two calls
  * that can run at the same time; 0 (and NULL allowed) for short histories.

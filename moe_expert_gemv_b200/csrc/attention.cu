@@ -17,9 +17,10 @@
 // (see attn_maps) are read by the four warps with 16-byte cp.async from
 // wherever the page table says.  Measured: 64 ragged sequences of up to 4096
 // tokens, 8 K/V heads of 128 (529 MB), 93 us, 5.7 TB/s; 2 of 100000, 4 K/V
-// heads (410 MB), 81 us, 5.1 TB/s (a plain reduction of as many bytes takes
+// heads (410 MB), 78 us, 5.2 TB/s (a plain reduction of as many bytes takes
 // 86); 2 of 400000, 6.3 TB/s; one of 900, 10 us, which is latency: lengths,
-// page table, cache, the joining of 16 CTAs' parts, one after the other.
+// page table, cache, the joining of up to 15 CTAs' parts, one after the other
+// (calls one after the other).
 #include "attn.cuh"
 
 namespace qmoe {

@@ -29,7 +29,9 @@
 // by 16-byte cp.async: 27 cycles per warp instruction, which held a 128-key
 // tile of K and V to 5200 cycles where the products need 2048.
 // Measured (of 1.65 PFLOP/s, counting visible pairs only): 4 ragged chunks of
-// 2048 tokens over 8192, 32 heads of 128, bf16, 336 us, 915 TFLOP/s -- a row
+// 2048 tokens over 8192, 32 heads of 128, bf16, 380 us, 810 TFLOP/s in calls one
+// after the other (power), 336, 915 TFLOP/s in one replay of a graph at a time,
+// as the other times here were taken -- a row
 // tile's chain (scores, softmax, weights, products) is as long as two row
 // tiles' products take, the tensor pipe is busy 47% of the time, the exponentials'
 // 47%.  A half row a softmax thread, four softmax warpgroups, made it 357 (80

@@ -23,7 +23,7 @@
 // A short history is looked through by every slice.  Where that is much work
 // (launch_tile) it is first sorted by ranges of slices, in a kernel of a CTA
 // per row that the slices' kernel overlaps (its logits do not wait for it).
-// Measured, 256 x 262144 bf16 with histories of up to 12000 tokens, a mask: 88
+// Measured, 256 x 262144 bf16 with histories of up to 12000 tokens, a mask: 86
 // us (44 without a history, which is 6.4 TB/s), of which the sort is the first
 // 15; then a slice's chain of loads (its range, its tokens, their logits) takes
 // 5 us, and 5 CTAs fit on an SM.  There the looking through unsorted histories

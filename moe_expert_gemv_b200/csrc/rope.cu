@@ -12,11 +12,12 @@
 // angle at position 10^6 would be off by 0.03 rad), the sine and cosine of
 // the reduced angle fp32.  A CTA is a token; what it waits for -- which
 // sequence, how long it is, which page -- is three loads in a row, so its
-// first two units per thread are on their way before.  Measured: 5325 tokens
-// of 32 + 8 + 8 heads of 128 (133 MB), 32.4 us, 4.1 TB/s (a plain elementwise
-// kernel over as many bytes: 24); 7 tokens 4.2 us.  The rest is the issue of
-// instructions, 74% of the cycles; CTAs of 128 threads take 31.0 at that size
-// but 6.2 instead of 4.2 for the 7 tokens.
+// first two units per thread are on their way before.  Measured, in a graph
+// of 20 calls: 5325 tokens of 32 + 8 + 8 heads of 128 (133 MB), 28.9 us, 4.6 TB/s
+// (a plain elementwise kernel over as many bytes: 24); 7 tokens 3.1 us; 5325
+// tokens' queries alone (87 MB), 19.4.  The rest is the issue of instructions,
+// 74% of the cycles.  One replay at a time CTAs of 128 threads took 31.0 in
+// place of 32.4 at that size but 6.2 in place of 4.2 for the 7 tokens.
 #include "attn.cuh"
 
 namespace qmoe {
