@@ -4,6 +4,7 @@
 
 #include <condition_variable>
 #include <mutex>
+#include <new>
 
 namespace qmoe {
 
@@ -50,16 +51,17 @@ private:
                 return true;
         return false;
     }
-    static std::mutex &mu()
+    // never destroyed: a thread may still wait here when the process ends, and
+    // destroying a condition waits for its waiters
+    template <class T>
+    static T &kept()
     {
-        static std::mutex m;
-        return m;
+        alignas(T) static unsigned char room[sizeof(T)];
+        static T *t = new (room) T;
+        return *t;
     }
-    static std::condition_variable &left()
-    {
-        static std::condition_variable c;
-        return c;
-    }
+    static std::mutex &mu() { return kept<std::mutex>(); }
+    static std::condition_variable &left() { return kept<std::condition_variable>(); }
     static LaunchTurn *&head()   // the calls that are launching, on their threads' stacks
     {
         static LaunchTurn *h = nullptr;

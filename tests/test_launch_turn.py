@@ -60,7 +60,12 @@ int main()
         });
     for (auto &t : threads)
         t.join();
-    return bad ? 4 : 0;
+    // the process ends although a call still launches and another waits for it
+    static int z = 0;
+    new LaunchTurn(&z);
+    std::thread([] { LaunchTurn t(&z); }).detach();
+    std::this_thread::sleep_for(std::chrono::milliseconds(50));
+    exit(bad ? 4 : 0);
 }
 """
 
