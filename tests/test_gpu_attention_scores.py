@@ -103,3 +103,16 @@ def test_the_widest_windows(cuda_dev, window, causal, max_new):
     out, lse = qmoe.attn_paged(c.cache, c.batch(max_new), c.q, window=window, causal=causal, want_lse=True)
     assert qmoe.qmoe_check_status() == 0
     c.check(out, lse, causal=causal)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 1e-30, 1e-44])
+@pytest.mark.parametrize("lens,heads,kv_heads,new", LENS, ids=["decode", "drafts", "chunks"])
+def test_caps_far_below_the_scores(cuda_dev, lens, heads, kv_heads, new, cap):
+    """Every score is plus or minus the cap, or 0 where the product is 0."""
+    c = Case(lens, heads, kv_heads, 128, 16, F16, seed=4)
+    for k in c.keys:
+        k[::3] = 0
+    c.write()
+    out = qmoe.attn_paged(c.cache, c.batch(new), c.q, softcap=cap)
+    assert qmoe.qmoe_check_status() == 0
+    check(c, out, 128 ** -0.5, cap, 2.0 ** -25)
